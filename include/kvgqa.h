@@ -15,6 +15,17 @@
  *   prefill_varlen_gqa_cached_rows_out_  prompts of different lengths at their
  *                                 own offsets (chunked prefill), same steps
  *
+ * and, over a cache whose rows are lists of pages of one pool:
+ *
+ *   paged_rope_kv_store_out_      RoPE with one or several position axes + K/V
+ *                                 store of packed new tokens into their pages
+ *   paged_gqa_attention_out_      GQA attention of a chunk of new tokens (or one)
+ *                                 of each sequence over its pages
+ *   paged_attention_mass_out_     attention weight of each cell from a chunk's
+ *                                 queries, added to what it has so far
+ *   paged_evict_out_              keeps each sequence's cells of greatest weight
+ *                                 and moves them to the front of its pages
+ *
  * Boundary conventions (same page, sections "Tensor ownership boundary" and
  * "Stable integration boundary"):
  *  - Every tensor crosses as a non-owning descriptor: pointer, accessible
@@ -112,6 +123,7 @@ typedef enum kvgqa_status {
 #define KVGQA_FLAG_POSITION_RANGE 0x1 /* some positions[a] outside [0, max_seq) */
 #define KVGQA_FLAG_ROW_RANGE 0x2      /* some cache_rows[a] outside [0, S) */
 #define KVGQA_FLAG_TIMEOUT 0x4        /* a bounded in-kernel wait expired; that work was dropped */
+#define KVGQA_FLAG_PAGE_RANGE 0x8     /* some block_table entry that was needed is outside [0, P) */
 
 /* Every workspace starts with a 256-byte status block; its first int32 is the
  * status word.  Kernels only OR bits into it.  It must be zero before first use
@@ -359,6 +371,157 @@ kvgqa_status prefill_varlen_gqa_cached_rows_out_(const kvgqa_tensor* q, const kv
                                                  double theta, float scale, const kvgqa_tensor* k_cache,
                                                  const kvgqa_tensor* v_cache, const kvgqa_tensor* out,
                                                  const kvgqa_tensor* workspace, void* stream);
+
+/*
+ * The paged cache.
+ *
+ * k_cache, v_cache [P, H_kv, page, D] are a pool of P pages of one layer.  Row a
+ * of block_table [A, max_pages] (int32) lists the pages of sequence a: its cell j
+ * is cell j % page of page block_table[a, j / page]; entries behind its last
+ * cell's are never read and may hold anything.  page is a power of two from 16
+ * to 256.  The new tokens of all sequences are packed: with query_starts [A + 1]
+ * (int32, not decreasing, query_starts[0] = 0) sequence a's are the rows
+ * query_starts[a] .. query_starts[a + 1] - 1 of a [N, ...] tensor, and with
+ * kv_lengths [A] (int32: its cells, the new tokens' included) they are its last
+ * cells.  Rows of the packed tensors from query_starts[A] on belong to no
+ * sequence: they are left as they are.  A sequence may have no new tokens.
+ * max_query_len is the caller's bound of the sequences' new tokens.
+ *
+ * Device-side checks: a sequence whose query_starts, kv_lengths or number of new
+ * tokens is out of range (negative or decreasing, past N, more new tokens than
+ * cells or than max_query_len, more cells than the table or the mass has) sets
+ * KVGQA_FLAG_POSITION_RANGE and is skipped: nothing of it is written.  A needed
+ * block_table entry outside [0, P) sets KVGQA_FLAG_PAGE_RANGE; no memory outside
+ * the pool is touched, other sequences are unaffected, and of that sequence the
+ * store skips the token, the eviction skips the sequence, and the attention's
+ * rows or masses have no meaning.
+ *
+ * Limits of the calls with attention in them: D in {64, 128}, G <= 16.
+ */
+
+/* Workspace of paged_rope_kv_store_out_: the status block. */
+kvgqa_status paged_rope_kv_store_workspace_size(size_t* bytes);
+
+/*
+ * paged_rope_kv_store_out_ -- RoPE with several position axes, and the store of
+ * the new tokens' K and V into their cells.
+ *
+ * For every packed token n of sequence a, whose cell is
+ * j = kv_lengths[a] - (query_starts[a + 1] - n):
+ *   q_out[n, h, :]         = RoPE(q[n, h, :])   for h < H_q
+ *   k_cache[cell j of a, g] = RoPE(k[n, g, :])  for g < H_kv
+ *   v_cache[cell j of a, g] = v[n, g, :]        (bytes copied unchanged)
+ * Pair i = (x[i], x[i + D/2]) of a head turns by the angle
+ * positions[axis_of_pair[i], n] * theta^(-2i/D).  One axis is ordinary RoPE; with
+ * three (time, height, width) the patches of an image or a video share positions
+ * that text never does, so a token's position and its cell are not tied: after
+ * an eviction they differ for text too.
+ *
+ *   q [N,H_q,D], k/v [N,H_kv,D] (each row contiguous; rows may lie further apart,
+ *     by any multiple of 8 elements, as views of a fused projection do)
+ *   positions [axes, N] int32, 1 <= axes <= 4, not negative (a token with a
+ *     negative position is skipped and KVGQA_FLAG_POSITION_RANGE set)
+ *   axis_of_pair  HOST array of D/2 bytes, each below axes (read by the call)
+ *   q_out [N,H_q,D] (written), k_cache/v_cache (one cell per token written)
+ *   workspace >= paged_rope_kv_store_workspace_size() bytes, 256-byte aligned
+ * Precondition: no two tokens of the call share a cell.  N = 0 is a no-op.
+ */
+kvgqa_status paged_rope_kv_store_out_(const kvgqa_tensor* q, const kvgqa_tensor* k, const kvgqa_tensor* v,
+                                      const kvgqa_tensor* positions, const kvgqa_tensor* query_starts,
+                                      const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table, double theta,
+                                      const uint8_t* axis_of_pair, const kvgqa_tensor* q_out,
+                                      const kvgqa_tensor* k_cache, const kvgqa_tensor* v_cache,
+                                      const kvgqa_tensor* workspace, void* stream);
+
+/* Workspace of paged_gqa_attention_out_ on `device`: the status block and the
+ * partial results of sequences that are split over the GPU (it depends on the
+ * device's SM count, not on the number or length of the sequences).  Nothing in
+ * it but the status word has to be zero before a call.  Calls that may overlap
+ * on the GPU need workspaces of their own. */
+kvgqa_status paged_gqa_attention_workspace_size(int64_t H_q, int64_t H_kv, int64_t D, int32_t device, size_t* bytes);
+
+/*
+ * paged_gqa_attention_out_ -- GQA attention of new tokens over a paged cache.
+ *
+ * For every packed token n of sequence a with cell j_n (as above), every query
+ * head h and g = floor(h / G):
+ *   out[n,h,:] = sum_{j=0..j_n} softmax_j( scale * q_rot[n,h,:] . k(a,g,j) ) * v(a,g,j)
+ *   lse[n,h]   = log sum_{j=0..j_n} exp( scale * q_rot[n,h,:] . k(a,g,j) )
+ * with k(a,g,j) the sequence's cell j: a token sees the cells up to its own, which
+ * the store wrote before.  One token per sequence is a decode step, many a chunk
+ * of a prompt; a call takes any mix.  Scores, softmax and sums are FP32, the
+ * weights enter the second product in the storage type, out is rounded once.
+ * Cells behind a sequence's last one weigh nothing whatever they hold; the
+ * sequence's own values have to be finite.
+ *
+ *   q_rot [N,H_q,D], k_cache/v_cache (read), scale finite
+ *   out [N,H_q,D] (written), lse [N,H_q] float32 (written; may be NULL)
+ *   workspace >= paged_gqa_attention_workspace_size(...) bytes, 256-byte aligned
+ * N = 0 or A = 0 is a no-op.
+ */
+kvgqa_status paged_gqa_attention_out_(const kvgqa_tensor* q_rot, const kvgqa_tensor* k_cache,
+                                      const kvgqa_tensor* v_cache, const kvgqa_tensor* query_starts,
+                                      const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table,
+                                      int64_t max_query_len, float scale, const kvgqa_tensor* out,
+                                      const kvgqa_tensor* lse, const kvgqa_tensor* workspace, void* stream);
+
+/* Workspace of paged_attention_mass_out_: the status block. */
+kvgqa_status paged_attention_mass_workspace_size(size_t* bytes);
+
+/*
+ * paged_attention_mass_out_ -- attention weight per cell, accumulated.
+ *
+ * For every sequence a with new tokens, KV head g and cell j < kv_lengths[a]:
+ *   mass[a,g,j] += sum over its tokens n with j <= j_n, and the G heads h of g, of
+ *                  exp( scale * q_rot[n,h,:] . k(a,g,j) - lse[n,h] )
+ * lse is the one paged_gqa_attention_out_ wrote for the same queries.  Called
+ * behind every step it gives the weight that each cell has drawn so far, called
+ * with a prompt's last tokens the weight of its cells for what comes next; both
+ * are what paged_evict_out_ chooses by.  The result does not depend on the run
+ * (no atomics).
+ *
+ *   q_rot [N,H_q,D], lse [N,H_q] float32, k_cache (read), scale finite
+ *   mass [A, H_kv, M] float32 (cells j < kv_lengths[a] of sequences with new
+ *     tokens updated; M >= every kv_lengths[a])
+ *   workspace >= paged_attention_mass_workspace_size() bytes, 256-byte aligned
+ */
+kvgqa_status paged_attention_mass_out_(const kvgqa_tensor* q_rot, const kvgqa_tensor* lse,
+                                       const kvgqa_tensor* k_cache, const kvgqa_tensor* query_starts,
+                                       const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table,
+                                       int64_t max_query_len, float scale, const kvgqa_tensor* mass,
+                                       const kvgqa_tensor* workspace, void* stream);
+
+/* Workspace of paged_evict_out_: the status block. */
+kvgqa_status paged_evict_workspace_size(int64_t A, int64_t H_kv, int64_t keep, size_t* bytes);
+
+/*
+ * paged_evict_out_ -- keep the cells of greatest mass.
+ *
+ * For every sequence a with n = kv_lengths[a] cells and every KV head g: where
+ * n > keep, the kept cells are the `recent` last ones and, of the n - recent
+ * others, the keep - recent of greatest mass[a,g,:] (equal masses: the lowest
+ * cells; NaN counts below every number); else all n.  With kept cells
+ * c_0 < c_1 < ... < c_{m-1}, m = min(n, keep):
+ *   kept[a,g,i]     = c_i for i < m, -1 behind
+ *   mass_out[a,g,i] = mass[a,g,c_i] for i < m, 0 behind (to M)
+ *   new_lengths[a]  = m
+ *   cell i of k_cache and v_cache, KV head g, takes what cell c_i held.
+ * The heads keep different cells but equally many, so the pages behind cell
+ * m - 1 are free.  Keys stay turned by the positions they were stored with, so a
+ * later token's position goes on from the sequence's, not from its cells.
+ *
+ *   mass [A, H_kv, M] float32, kv_lengths [A], block_table [A, max_pages] (read)
+ *   keep >= 1, 0 <= recent <= keep
+ *   k_cache/v_cache [P, H_kv, page, D] (cells moved in place)
+ *   mass_out [A, H_kv, M] float32, kept [A, H_kv, keep] int32, new_lengths [A] int32
+ *   workspace >= paged_evict_workspace_size(...) bytes, 256-byte aligned
+ * Precondition: a page whose cells move belongs to one sequence, once.
+ */
+kvgqa_status paged_evict_out_(const kvgqa_tensor* mass, const kvgqa_tensor* kv_lengths,
+                              const kvgqa_tensor* block_table, int64_t keep, int64_t recent,
+                              const kvgqa_tensor* k_cache, const kvgqa_tensor* v_cache, const kvgqa_tensor* mass_out,
+                              const kvgqa_tensor* kept, const kvgqa_tensor* new_lengths,
+                              const kvgqa_tensor* workspace, void* stream);
 
 /*
  * Slot table and step metadata (host side, no kernels).

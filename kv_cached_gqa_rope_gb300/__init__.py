@@ -14,6 +14,17 @@ Functions keep the names of the C entry points:
     prefill_varlen_gqa_cached_rows_out_(q, k, v, offsets, lengths, cache_rows, theta, scale,
                                         k_cache, v_cache, out, workspace)
 
+and, over a paged cache (one pool of pages, a block table per sequence):
+
+    paged_rope_kv_store_out_(q, k, v, positions, query_starts, kv_lengths, block_table, theta,
+                             axis_of_pair, q_out, k_cache, v_cache, workspace)
+    paged_gqa_attention_out_(q_rot, k_cache, v_cache, query_starts, kv_lengths, block_table,
+                             max_query_len, scale, out, lse, workspace)
+    paged_attention_mass_out_(q_rot, lse, k_cache, query_starts, kv_lengths, block_table,
+                              max_query_len, scale, mass, workspace)
+    paged_evict_out_(mass, kv_lengths, block_table, keep, recent, k_cache, v_cache, mass_out, kept,
+                     new_lengths, workspace)
+
 plus the workspace-size queries and ``kvgqa_read_status``.  Shapes, layouts
 and the meaning of every argument are documented in ``include/kvgqa.h``.
 """
@@ -30,7 +41,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libkvgqa.so")
 KVGQA_BF16, KVGQA_I32, KVGQA_F32, KVGQA_U8, KVGQA_F16 = 1, 2, 3, 4, 5
 STATUS_NAMES = {0: "OK", 1: "EINVAL", 2: "EDTYPE", 3: "ELAYOUT", 4: "EDEVICE", 5: "EALIAS",
                 6: "EWORKSPACE", 7: "ECUDA", 8: "EUNSUPPORTED", 9: "EFULL"}
-FLAG_POSITION_RANGE, FLAG_ROW_RANGE, FLAG_TIMEOUT = 0x1, 0x2, 0x4
+FLAG_POSITION_RANGE, FLAG_ROW_RANGE, FLAG_TIMEOUT, FLAG_PAGE_RANGE = 0x1, 0x2, 0x4, 0x8
 STATUS_BYTES = 256
 _DTYPES = {torch.bfloat16: KVGQA_BF16, torch.int32: KVGQA_I32, torch.float32: KVGQA_F32,
            torch.uint8: KVGQA_U8, torch.float16: KVGQA_F16}
@@ -94,6 +105,18 @@ def _load():
     for name in ("kvgqa_slots_create", "kvgqa_slots_destroy", "kvgqa_slots_admit", "kvgqa_slots_release",
                  "kvgqa_slots_step", "kvgqa_slots_query", "kvgqa_metadata_upload"):
         getattr(lib, name).restype = st
+    I64, SZ = ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)
+    lib.paged_rope_kv_store_workspace_size.argtypes = [SZ]
+    lib.paged_rope_kv_store_out_.argtypes = [P] * 7 + [ctypes.c_double, ctypes.c_char_p] + [P] * 4 + [VP]
+    lib.paged_gqa_attention_workspace_size.argtypes = [I64] * 3 + [ctypes.c_int32, SZ]
+    lib.paged_gqa_attention_out_.argtypes = [P] * 6 + [I64, ctypes.c_float] + [P] * 3 + [VP]
+    lib.paged_attention_mass_workspace_size.argtypes = [SZ]
+    lib.paged_attention_mass_out_.argtypes = [P] * 6 + [I64, ctypes.c_float] + [P] * 2 + [VP]
+    lib.paged_evict_workspace_size.argtypes = [I64] * 3 + [SZ]
+    lib.paged_evict_out_.argtypes = [P] * 3 + [I64] * 2 + [P] * 6 + [VP]
+    for name in ("paged_rope_kv_store", "paged_gqa_attention", "paged_attention_mass", "paged_evict"):
+        getattr(lib, name + "_workspace_size").restype = st
+        getattr(lib, name + "_out_").restype = st
     lib.kvgqa_read_status.argtypes = [P, ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
     lib.kvgqa_read_status.restype = st
     lib.kvgqa_check_bounded_wait.argtypes = [P, ctypes.c_void_p]
@@ -111,7 +134,10 @@ EXPORTED_SYMBOLS = ("kvgqa_abi_version", "kvgqa_last_error", "rope_kv_store_work
                     "decode_step_out_", "kvgqa_slots_create", "kvgqa_slots_destroy", "kvgqa_slots_admit",
                     "kvgqa_slots_release", "kvgqa_slots_step", "kvgqa_slots_query", "kvgqa_metadata_upload",
                     "prefill_varlen_gqa_cached_rows_out_", "decode_step_single_launch_out_",
-                    "kvgqa_check_bounded_wait")
+                    "kvgqa_check_bounded_wait", "paged_rope_kv_store_workspace_size", "paged_rope_kv_store_out_",
+                    "paged_gqa_attention_workspace_size", "paged_gqa_attention_out_",
+                    "paged_attention_mass_workspace_size", "paged_attention_mass_out_",
+                    "paged_evict_workspace_size", "paged_evict_out_")
 
 
 def library() -> ctypes.CDLL:
@@ -304,6 +330,123 @@ def prepare_prefill_varlen_gqa_cached_rows_out_(q, k, v, offsets, lengths, cache
             ctypes.c_void_p(_stream(stream)))
     return Prepared(_lib.prefill_varlen_gqa_cached_rows_out_, args,
                     (ds, q, k, v, offsets, lengths, cache_rows, k_cache, v_cache, out, workspace))
+
+
+# ---------------------------------------------------------------- paged cache
+def rope_axis_of_pair(sections, interleaved=False) -> list:
+    """The position axis of each of a head's D/2 rotary pairs, for
+    paged_rope_kv_store_out_: `sections[x]` pairs turn by axis x, as runs, or by
+    turns (0, 1, 2, 0, 1, 2, ...) until an axis has all of its pairs."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0:
+        raise ValueError("sections must be counts of pairs")
+    if not interleaved:
+        return [x for x, n in enumerate(left) for _ in range(n)]
+    out = []
+    while any(left):
+        for x, n in enumerate(left):
+            if n:
+                left[x] -= 1
+                out.append(x)
+    return out
+
+
+def paged_rope_kv_store_workspace_size() -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.paged_rope_kv_store_workspace_size(ctypes.byref(n)))
+    return n.value
+
+
+def paged_gqa_attention_workspace_size(H_q: int, H_kv: int, D: int, device: int = None) -> int:
+    if device is None:
+        device = torch.cuda.current_device()
+    n = ctypes.c_size_t()
+    _check(_lib.paged_gqa_attention_workspace_size(H_q, H_kv, D, device, ctypes.byref(n)))
+    return n.value
+
+
+def paged_attention_mass_workspace_size() -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.paged_attention_mass_workspace_size(ctypes.byref(n)))
+    return n.value
+
+
+def paged_evict_workspace_size(A: int, H_kv: int, keep: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.paged_evict_workspace_size(A, H_kv, keep, ctypes.byref(n)))
+    return n.value
+
+
+def prepare_paged_rope_kv_store_out_(q, k, v, positions, query_starts, kv_lengths, block_table, theta, axis_of_pair,
+                                     q_out, k_cache, v_cache, workspace, stream=None) -> Prepared:
+    axis = bytes(axis_of_pair)
+    if len(axis) != q.shape[-1] // 2:
+        raise ValueError(f"axis_of_pair has {len(axis)} entries, expected D/2 = {q.shape[-1] // 2}")
+    keep = (q, k, v, positions, query_starts, kv_lengths, block_table, q_out, k_cache, v_cache, workspace)
+    ds = [describe(t) for t in keep]
+    args = (*map(_ref, ds[:7]), ctypes.c_double(theta), ctypes.c_char_p(axis), *map(_ref, ds[7:]),
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared(_lib.paged_rope_kv_store_out_, args, (ds, axis, keep))
+
+
+def prepare_paged_gqa_attention_out_(q_rot, k_cache, v_cache, query_starts, kv_lengths, block_table, max_query_len,
+                                     scale, out, lse, workspace, stream=None) -> Prepared:
+    keep = (q_rot, k_cache, v_cache, query_starts, kv_lengths, block_table, out, lse, workspace)
+    ds = [None if t is None else describe(t) for t in keep]
+    refs = [None if d is None else _ref(d) for d in ds]
+    args = (*refs[:6], ctypes.c_int64(max_query_len), ctypes.c_float(scale), *refs[6:],
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared(_lib.paged_gqa_attention_out_, args, (ds, keep))
+
+
+def prepare_paged_attention_mass_out_(q_rot, lse, k_cache, query_starts, kv_lengths, block_table, max_query_len,
+                                      scale, mass, workspace, stream=None) -> Prepared:
+    keep = (q_rot, lse, k_cache, query_starts, kv_lengths, block_table, mass, workspace)
+    ds = [describe(t) for t in keep]
+    args = (*map(_ref, ds[:6]), ctypes.c_int64(max_query_len), ctypes.c_float(scale), *map(_ref, ds[6:]),
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared(_lib.paged_attention_mass_out_, args, (ds, keep))
+
+
+def prepare_paged_evict_out_(mass, kv_lengths, block_table, keep, recent, k_cache, v_cache, mass_out, kept,
+                             new_lengths, workspace, stream=None) -> Prepared:
+    held = (mass, kv_lengths, block_table, k_cache, v_cache, mass_out, kept, new_lengths, workspace)
+    ds = [describe(t) for t in held]
+    args = (*map(_ref, ds[:3]), ctypes.c_int64(keep), ctypes.c_int64(recent), *map(_ref, ds[3:]),
+            ctypes.c_void_p(_stream(stream)))
+    return Prepared(_lib.paged_evict_out_, args, (ds, held))
+
+
+def paged_rope_kv_store_out_(q, k, v, positions, query_starts, kv_lengths, block_table, theta, axis_of_pair, q_out,
+                             k_cache, v_cache, workspace, stream=None) -> None:
+    """RoPE of packed new tokens, pair i by the position on axis
+    axis_of_pair[i] (see rope_axis_of_pair), and the store of K and V into
+    each token's cell of its sequence's pages."""
+    prepare_paged_rope_kv_store_out_(q, k, v, positions, query_starts, kv_lengths, block_table, theta, axis_of_pair,
+                                     q_out, k_cache, v_cache, workspace, stream)()
+
+
+def paged_gqa_attention_out_(q_rot, k_cache, v_cache, query_starts, kv_lengths, block_table, max_query_len, scale,
+                             out, lse, workspace, stream=None) -> None:
+    """Attention of packed new tokens over their sequences' pages; `lse` (the
+    log of each softmax's sum) may be None."""
+    prepare_paged_gqa_attention_out_(q_rot, k_cache, v_cache, query_starts, kv_lengths, block_table, max_query_len,
+                                     scale, out, lse, workspace, stream)()
+
+
+def paged_attention_mass_out_(q_rot, lse, k_cache, query_starts, kv_lengths, block_table, max_query_len, scale, mass,
+                              workspace, stream=None) -> None:
+    """Adds the attention weight that each cell gets from these queries to `mass`."""
+    prepare_paged_attention_mass_out_(q_rot, lse, k_cache, query_starts, kv_lengths, block_table, max_query_len,
+                                      scale, mass, workspace, stream)()
+
+
+def paged_evict_out_(mass, kv_lengths, block_table, keep, recent, k_cache, v_cache, mass_out, kept, new_lengths,
+                     workspace, stream=None) -> None:
+    """Keeps each KV head's `recent` last cells and those of greatest mass,
+    `keep` in all, at the front of the sequence's pages."""
+    prepare_paged_evict_out_(mass, kv_lengths, block_table, keep, recent, k_cache, v_cache, mass_out, kept,
+                             new_lengths, workspace, stream)()
 
 
 def kvgqa_read_status(workspace, stream=None) -> int:

@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG_DIR, "libkvgqa.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "rope_kv_store.cu", "flash_decode.cu", "flash_decode_f16.cu", "prefill_attention.cu",
-           "wait_check.cu"]
+           "paged_store.cu", "paged_attention.cu", "paged_mass.cu", "paged_evict.cu", "wait_check.cu"]
 
 
 def nvcc_path() -> str:

@@ -765,6 +765,349 @@ kvgqa_status prefill_varlen_gqa_cached_rows_out_(const kvgqa_tensor* q, const kv
   });
 }
 
+}  // extern "C"
+
+namespace {
+
+// ---------------------------------------------------------------- paged cache
+struct PagedViews {
+  View starts, lengths, table;
+};
+
+// page of a pool [P, H_kv, page, D]: a power of two from 16 to 256.
+int page_shift_of(int64_t page) {
+  for (int s = 4; s <= 8; ++s)
+    if (page == (1 << s)) return s;
+  fail(page <= 0 ? KVGQA_EINVAL : KVGQA_EUNSUPPORTED, "page=%lld: kernels exist for powers of two from 16 to 256",
+       (long long)page);
+}
+
+// The pool's sizes and the metadata shared by the paged calls.  query_starts is
+// null for the eviction, which has no queries (N and max_query_len 0).
+PagedViews paged_meta(kvgqa::PagedMeta* m, const kvgqa_tensor* query_starts, bool queries,
+                      const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table, int64_t N,
+                      int64_t max_query_len, const kvgqa_tensor* k_cache) {
+  PagedViews v;
+  v.lengths = check_tensor("kv_lengths", kv_lengths, 1, KVGQA_I32, 4);
+  v.table = check_tensor("block_table", block_table, 2, KVGQA_I32, 4);
+  const int64_t A = kv_lengths->shape[0], max_pages = block_table->shape[1];
+  require_shape(v.table, {A, max_pages});
+  if (queries) {
+    v.starts = check_tensor("query_starts", query_starts, 1, KVGQA_I32, 4);
+    require_shape(v.starts, {A + 1});
+  }
+  if (max_query_len < 0) fail(KVGQA_EINVAL, "max_query_len < 0");
+  const int64_t P = k_cache->shape[0], H_kv = k_cache->shape[1], page = k_cache->shape[2];
+  const int shift = page_shift_of(page);
+  if (N > (1ll << 30) || A > (1ll << 30)) fail(KVGQA_EUNSUPPORTED, "more than 2^30 tokens or sequences");
+  if (!product_below({P, H_kv}, 1ll << 31)) fail(KVGQA_EUNSUPPORTED, "P*H_kv must stay below 2^31");
+  if (!product_below({max_pages, page}, (1ll << 30) + 1)) fail(KVGQA_EUNSUPPORTED, "max_pages*page must not exceed 2^30");
+  m->A = (int)A;
+  m->N = (int)N;
+  m->max_query_len = (int)(max_query_len < N ? max_query_len : N);
+  m->max_pages = (int)max_pages;
+  m->max_cells = (int)(max_pages * page);
+  m->page_shift = shift;
+  m->P = (int)P;
+  m->query_starts = queries ? static_cast<const int32_t*>(query_starts->data) : nullptr;
+  m->kv_lengths = static_cast<const int32_t*>(kv_lengths->data);
+  m->block_table = static_cast<const int32_t*>(block_table->data);
+  return v;
+}
+
+// Whether the schedule's units of a paged attention call (about one per key
+// tile and block of queries; see the kernels) stay below 2^30, whatever the
+// sequences: N tokens in blocks of at least `block`, one more per sequence, each
+// over all of a sequence's cells.
+void check_paged_work(const kvgqa::PagedMeta& m, int64_t H_kv, int64_t block) {
+  const int64_t blocks = m.N / block + m.A, units = m.max_cells / 128 + m.max_query_len / 128 + 8;
+  if (!product_below({blocks, units, H_kv}, 1ll << 30))
+    fail(KVGQA_EUNSUPPORTED, "too much work for one call (tokens, cells and heads); split the batch");
+}
+
+int padded_group(int64_t H_q, int64_t H_kv) {
+  check_heads(H_q, H_kv);
+  const int64_t G = H_q / H_kv;
+  if (G > 16) fail(KVGQA_EUNSUPPORTED, "group size %lld: kernels cover G <= 16", (long long)G);
+  return kvgqa::decode_group_pad((int)G);
+}
+
+// A token-major view [N, H, D] whose rows (tokens) may lie further apart than
+// H * D elements, by a multiple of 8.
+View check_token_rows(const char* name, const kvgqa_tensor* t, int64_t N, int64_t H, int64_t D, int32_t elem,
+                      int64_t* stride) {
+  if (!t) fail(KVGQA_EINVAL, "%s: null descriptor", name);
+  if (t->ndim != 3) fail(KVGQA_EINVAL, "%s: expected rank 3, got %d", name, t->ndim);
+  if (t->dtype != elem) fail(KVGQA_EDTYPE, "%s: expected %s, got %s", name, dtype_name(elem), dtype_name(t->dtype));
+  View v{name, t};
+  require_shape(v, {N, H, D});
+  if (N == 0) return v;
+  if ((D > 1 && t->strides[2] != 1) || (H > 1 && t->strides[1] != D))
+    fail(KVGQA_ELAYOUT, "%s: a token's heads must be contiguous", name);
+  *stride = N > 1 ? t->strides[0] : H * D;
+  if (*stride < H * D || *stride % 8) fail(KVGQA_ELAYOUT, "%s: tokens must lie at least H*D elements apart, by a multiple of 8", name);
+  int64_t bytes = 0;
+  if (__builtin_mul_overflow(N - 1, *stride, &bytes) || __builtin_add_overflow(bytes, H * D, &bytes) ||
+      __builtin_mul_overflow(bytes, static_cast<int64_t>(2), &bytes))
+    fail(KVGQA_EINVAL, "%s: sizes overflow a 64-bit byte count", name);
+  if (!t->data) fail(KVGQA_EINVAL, "%s: null data", name);
+  if (t->bytes < bytes)
+    fail(KVGQA_EINVAL, "%s: view needs %lld bytes, descriptor allows %lld", name, (long long)bytes, (long long)t->bytes);
+  if (reinterpret_cast<uintptr_t>(t->data) % 16) fail(KVGQA_ELAYOUT, "%s: data pointer not 16-byte aligned", name);
+  v.lo = reinterpret_cast<uintptr_t>(t->data);
+  v.hi = v.lo + static_cast<uintptr_t>(bytes);
+  return v;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvgqa_status paged_rope_kv_store_workspace_size(size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(KVGQA_EINVAL, "bytes: null");
+    *bytes = KVGQA_STATUS_BYTES;
+  });
+}
+
+kvgqa_status paged_rope_kv_store_out_(const kvgqa_tensor* q, const kvgqa_tensor* k, const kvgqa_tensor* v,
+                                      const kvgqa_tensor* positions, const kvgqa_tensor* query_starts,
+                                      const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table, double theta,
+                                      const uint8_t* axis_of_pair, const kvgqa_tensor* q_out,
+                                      const kvgqa_tensor* k_cache, const kvgqa_tensor* v_cache,
+                                      const kvgqa_tensor* workspace, void* stream) {
+  return guarded([&] {
+    if (!q || !k_cache || !positions) fail(KVGQA_EINVAL, "null descriptor");
+    if (q->ndim != 3 || k_cache->ndim != 4) fail(KVGQA_EINVAL, "q must be [N,H_q,D], caches [P,H_kv,page,D]");
+    const int64_t N = q->shape[0], H_q = q->shape[1], D = q->shape[2];
+    const int64_t P = k_cache->shape[0], H_kv = k_cache->shape[1], page = k_cache->shape[2];
+    check_head_dim(D);
+    check_heads(H_q, H_kv);
+    check_theta(theta);
+    if (H_q > (1 << 20)) fail(KVGQA_EUNSUPPORTED, "H_q=%lld", (long long)H_q);
+    const int32_t elem = storage_type(q, "q");
+    kvgqa::PagedStoreParams p{};
+    View vkc = check_tensor("k_cache", k_cache, 4, elem, 16);
+    View vvc = check_tensor("v_cache", v_cache, 4, elem, 16);
+    require_shape(vkc, {P, H_kv, page, D});
+    require_shape(vvc, {P, H_kv, page, D});
+    View vq = check_token_rows("q", q, N, H_q, D, elem, &p.q_stride);
+    View vk = check_token_rows("k", k, N, H_kv, D, elem, &p.k_stride);
+    View vv = check_token_rows("v", v, N, H_kv, D, elem, &p.v_stride);
+    PagedViews pv = paged_meta(&p.m, query_starts, true, kv_lengths, block_table, N, N, k_cache);
+    View vp = check_tensor("positions", positions, 2, KVGQA_I32, 4);
+    const int64_t axes = positions->shape[0];
+    if (axes < 1 || axes > 4) fail(KVGQA_EINVAL, "positions: %lld axes, expected 1 to 4", (long long)axes);
+    require_shape(vp, {axes, N});
+    View vqo = check_tensor("q_out", q_out, 3, elem, 16);
+    require_shape(vqo, {N, H_q, D});
+    if (!axis_of_pair) fail(KVGQA_EINVAL, "axis_of_pair: null");
+    for (int64_t i = 0; i < D / 2; ++i) {
+      if (axis_of_pair[i] >= axes)
+        fail(KVGQA_EINVAL, "axis_of_pair[%lld] = %d, expected below %lld", (long long)i, axis_of_pair[i], (long long)axes);
+      p.axis[i] = axis_of_pair[i];
+    }
+    View vws = check_workspace(workspace, KVGQA_STATUS_BYTES);
+    const std::initializer_list<const View*> all = {&vq, &vk, &vv, &vp, &pv.starts, &pv.lengths, &pv.table, &vqo, &vkc, &vvc, &vws};
+    check_no_alias({&vqo, &vkc, &vvc, &vws}, all);
+    check_device(all, current_device());
+    if (N == 0 || p.m.A == 0) return;
+    p.q = static_cast<const uint16_t*>(q->data);
+    p.k = static_cast<const uint16_t*>(k->data);
+    p.v = static_cast<const uint16_t*>(v->data);
+    p.positions = static_cast<const int32_t*>(positions->data);
+    p.q_out = static_cast<uint16_t*>(q_out->data);
+    p.k_cache = static_cast<uint16_t*>(k_cache->data);
+    p.v_cache = static_cast<uint16_t*>(v_cache->data);
+    p.status = static_cast<int32_t*>(workspace->data);
+    p.H_q = (int)H_q; p.H_kv = (int)H_kv; p.D = (int)D;
+    p.f16 = elem == KVGQA_F16;
+    fill_rope_freqs(&p.freqs, (int)D, theta);
+    check_cuda(kvgqa::launch_paged_rope_kv_store(p, static_cast<cudaStream_t>(stream)), "paged_rope_kv_store launch");
+  });
+}
+
+kvgqa_status paged_gqa_attention_workspace_size(int64_t H_q, int64_t H_kv, int64_t D, int32_t device, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(KVGQA_EINVAL, "bytes: null");
+    check_head_dim(D);
+    padded_group(H_q, H_kv);
+    kvgqa::PagedLayout lay;
+    check_cuda(kvgqa::paged_attention_layout(device, (int)D, &lay), "paged attention set-up");
+    *bytes = KVGQA_STATUS_BYTES + lay.cut_bytes + lay.partial_bytes;
+  });
+}
+
+kvgqa_status paged_gqa_attention_out_(const kvgqa_tensor* q_rot, const kvgqa_tensor* k_cache,
+                                      const kvgqa_tensor* v_cache, const kvgqa_tensor* query_starts,
+                                      const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table,
+                                      int64_t max_query_len, float scale, const kvgqa_tensor* out,
+                                      const kvgqa_tensor* lse, const kvgqa_tensor* workspace, void* stream) {
+  return guarded([&] {
+    if (!q_rot || !k_cache) fail(KVGQA_EINVAL, "null descriptor");
+    if (q_rot->ndim != 3 || k_cache->ndim != 4) fail(KVGQA_EINVAL, "q_rot must be [N,H_q,D], caches [P,H_kv,page,D]");
+    const int64_t N = q_rot->shape[0], H_q = q_rot->shape[1], D = q_rot->shape[2];
+    const int64_t P = k_cache->shape[0], H_kv = k_cache->shape[1], page = k_cache->shape[2];
+    check_head_dim(D);
+    const int gp = padded_group(H_q, H_kv);
+    if (!std::isfinite(scale)) fail(KVGQA_EINVAL, "scale must be finite");
+    const int32_t elem = storage_type(q_rot, "q_rot");
+    kvgqa::PagedAttentionParams p{};
+    View vq = check_tensor("q_rot", q_rot, 3, elem, 16);
+    View vkc = check_tensor("k_cache", k_cache, 4, elem, 16);
+    View vvc = check_tensor("v_cache", v_cache, 4, elem, 16);
+    require_shape(vkc, {P, H_kv, page, D});
+    require_shape(vvc, {P, H_kv, page, D});
+    PagedViews pv = paged_meta(&p.m, query_starts, true, kv_lengths, block_table, N, max_query_len, k_cache);
+    check_paged_work(p.m, H_kv, 256 / gp);
+    View vo = check_tensor("out", out, 3, elem, 16);
+    require_shape(vo, {N, H_q, D});
+    View vl{"lse", nullptr};
+    if (lse) {
+      vl = check_tensor("lse", lse, 2, KVGQA_F32, 4);
+      require_shape(vl, {N, H_q});
+    }
+    View vws0 = check_workspace(workspace, KVGQA_STATUS_BYTES);
+    check_no_alias({&vo, &vl, &vws0}, {&vq, &vkc, &vvc, &pv.starts, &pv.lengths, &pv.table, &vo, &vl, &vws0});
+    const int dev = current_device();
+    kvgqa::PagedLayout lay;
+    check_cuda(kvgqa::paged_attention_layout(dev, (int)D, &lay), "paged attention set-up");
+    View vws = check_workspace(workspace, KVGQA_STATUS_BYTES + lay.cut_bytes + lay.partial_bytes);
+    check_device({&vq, &vkc, &vvc, &pv.starts, &pv.lengths, &pv.table, &vo, &vl, &vws}, dev);
+    if (N == 0 || p.m.A == 0) return;
+    if (P == 0) fail(KVGQA_EINVAL, "k_cache: the pool has no page");
+    unsigned char* ws = static_cast<unsigned char*>(workspace->data);
+    p.q = static_cast<const uint16_t*>(q_rot->data);
+    p.k_cache = static_cast<const uint16_t*>(k_cache->data);
+    p.v_cache = static_cast<const uint16_t*>(v_cache->data);
+    p.out = static_cast<uint16_t*>(out->data);
+    p.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+    p.status = reinterpret_cast<int32_t*>(ws);
+    p.cuts = ws + KVGQA_STATUS_BYTES;
+    p.partials = reinterpret_cast<float*>(ws + KVGQA_STATUS_BYTES + lay.cut_bytes);
+    p.H_q = (int)H_q; p.H_kv = (int)H_kv; p.G = (int)(H_q / H_kv); p.D = (int)D;
+    p.f16 = elem == KVGQA_F16;
+    p.num_ctas = lay.num_ctas;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    check_cuda(kvgqa::launch_paged_attention(p, static_cast<cudaStream_t>(stream)), "paged_gqa_attention launch");
+  });
+}
+
+kvgqa_status paged_attention_mass_workspace_size(size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(KVGQA_EINVAL, "bytes: null");
+    *bytes = KVGQA_STATUS_BYTES;
+  });
+}
+
+kvgqa_status paged_attention_mass_out_(const kvgqa_tensor* q_rot, const kvgqa_tensor* lse,
+                                       const kvgqa_tensor* k_cache, const kvgqa_tensor* query_starts,
+                                       const kvgqa_tensor* kv_lengths, const kvgqa_tensor* block_table,
+                                       int64_t max_query_len, float scale, const kvgqa_tensor* mass,
+                                       const kvgqa_tensor* workspace, void* stream) {
+  return guarded([&] {
+    if (!q_rot || !k_cache || !mass) fail(KVGQA_EINVAL, "null descriptor");
+    if (q_rot->ndim != 3 || k_cache->ndim != 4) fail(KVGQA_EINVAL, "q_rot must be [N,H_q,D], caches [P,H_kv,page,D]");
+    const int64_t N = q_rot->shape[0], H_q = q_rot->shape[1], D = q_rot->shape[2];
+    const int64_t P = k_cache->shape[0], H_kv = k_cache->shape[1];
+    check_head_dim(D);
+    const int gp = padded_group(H_q, H_kv);
+    if (!std::isfinite(scale)) fail(KVGQA_EINVAL, "scale must be finite");
+    const int32_t elem = storage_type(q_rot, "q_rot");
+    kvgqa::PagedMassParams p{};
+    View vq = check_tensor("q_rot", q_rot, 3, elem, 16);
+    View vl = check_tensor("lse", lse, 2, KVGQA_F32, 4);
+    require_shape(vl, {N, H_q});
+    View vkc = check_tensor("k_cache", k_cache, 4, elem, 16);
+    require_shape(vkc, {P, H_kv, k_cache->shape[2], D});
+    PagedViews pv = paged_meta(&p.m, query_starts, true, kv_lengths, block_table, N, max_query_len, k_cache);
+    check_paged_work(p.m, H_kv, 128 / gp);
+    View vm = check_tensor("mass", mass, 3, KVGQA_F32, 4);
+    const int64_t M = mass->shape[2];
+    require_shape(vm, {p.m.A, H_kv, M});
+    if (M > (1ll << 30)) fail(KVGQA_EUNSUPPORTED, "mass: more than 2^30 cells");
+    View vws = check_workspace(workspace, KVGQA_STATUS_BYTES);
+    const std::initializer_list<const View*> all = {&vq, &vl, &vkc, &pv.starts, &pv.lengths, &pv.table, &vm, &vws};
+    check_no_alias({&vm, &vws}, all);
+    const int dev = current_device();
+    check_device(all, dev);
+    kvgqa::PagedLayout lay;
+    check_cuda(kvgqa::paged_attention_layout(dev, (int)D, &lay), "paged attention set-up");
+    if (N == 0 || p.m.A == 0) return;
+    if (P == 0) fail(KVGQA_EINVAL, "k_cache: the pool has no page");
+    if (M < p.m.max_cells) p.m.max_cells = (int)M;
+    p.q = static_cast<const uint16_t*>(q_rot->data);
+    p.lse = static_cast<const float*>(lse->data);
+    p.k_cache = static_cast<const uint16_t*>(k_cache->data);
+    p.mass = static_cast<float*>(mass->data);
+    p.status = static_cast<int32_t*>(workspace->data);
+    p.H_q = (int)H_q; p.H_kv = (int)H_kv; p.G = (int)(H_q / H_kv); p.D = (int)D;
+    p.f16 = elem == KVGQA_F16;
+    p.num_ctas = lay.num_ctas;
+    p.mass_cells = (int)M;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    check_cuda(kvgqa::launch_paged_mass(p, static_cast<cudaStream_t>(stream)), "paged_attention_mass launch");
+  });
+}
+
+kvgqa_status paged_evict_workspace_size(int64_t A, int64_t H_kv, int64_t keep, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(KVGQA_EINVAL, "bytes: null");
+    if (A < 0 || H_kv <= 0 || keep < 1) fail(KVGQA_EINVAL, "A=%lld, H_kv=%lld, keep=%lld", (long long)A, (long long)H_kv, (long long)keep);
+    *bytes = KVGQA_STATUS_BYTES;
+  });
+}
+
+kvgqa_status paged_evict_out_(const kvgqa_tensor* mass, const kvgqa_tensor* kv_lengths,
+                              const kvgqa_tensor* block_table, int64_t keep, int64_t recent,
+                              const kvgqa_tensor* k_cache, const kvgqa_tensor* v_cache, const kvgqa_tensor* mass_out,
+                              const kvgqa_tensor* kept, const kvgqa_tensor* new_lengths,
+                              const kvgqa_tensor* workspace, void* stream) {
+  return guarded([&] {
+    if (!mass || !k_cache) fail(KVGQA_EINVAL, "null descriptor");
+    if (k_cache->ndim != 4) fail(KVGQA_EINVAL, "caches must be [P,H_kv,page,D]");
+    const int64_t P = k_cache->shape[0], H_kv = k_cache->shape[1], page = k_cache->shape[2], D = k_cache->shape[3];
+    check_head_dim(D);
+    check_heads(H_kv, H_kv);
+    if (keep < 1 || recent < 0 || recent > keep)
+      fail(KVGQA_EINVAL, "keep=%lld must be positive and recent=%lld in [0, keep]", (long long)keep, (long long)recent);
+    if (keep > (1ll << 30)) fail(KVGQA_EUNSUPPORTED, "keep: more than 2^30 cells");
+    const int32_t elem = storage_type(k_cache, "k_cache");
+    kvgqa::PagedEvictParams p{};
+    View vkc = check_tensor("k_cache", k_cache, 4, elem, 16);
+    View vvc = check_tensor("v_cache", v_cache, 4, elem, 16);
+    require_shape(vvc, {P, H_kv, page, D});
+    PagedViews pv = paged_meta(&p.m, nullptr, false, kv_lengths, block_table, 0, 0, k_cache);
+    const int64_t A = p.m.A;
+    View vm = check_tensor("mass", mass, 3, KVGQA_F32, 4);
+    const int64_t M = mass->shape[2];
+    if (M > (1ll << 30)) fail(KVGQA_EUNSUPPORTED, "mass: more than 2^30 cells");
+    require_shape(vm, {A, H_kv, M});
+    View vmo = check_tensor("mass_out", mass_out, 3, KVGQA_F32, 4);
+    require_shape(vmo, {A, H_kv, M});
+    View vk = check_tensor("kept", kept, 3, KVGQA_I32, 4);
+    require_shape(vk, {A, H_kv, keep});
+    View vn = check_tensor("new_lengths", new_lengths, 1, KVGQA_I32, 4);
+    require_shape(vn, {A});
+    if (!product_below({A, H_kv, 16}, 1ll << 31)) fail(KVGQA_EUNSUPPORTED, "A*H_kv must stay below 2^27");
+    View vws = check_workspace(workspace, KVGQA_STATUS_BYTES);
+    const std::initializer_list<const View*> all = {&vm, &pv.lengths, &pv.table, &vkc, &vvc, &vmo, &vk, &vn, &vws};
+    check_no_alias({&vkc, &vvc, &vmo, &vk, &vn, &vws}, all);
+    check_device(all, current_device());
+    if (A == 0) return;
+    if (M < p.m.max_cells) p.m.max_cells = (int)M;
+    p.mass = static_cast<const float*>(mass->data);
+    p.k_cache = static_cast<uint16_t*>(k_cache->data);
+    p.v_cache = static_cast<uint16_t*>(v_cache->data);
+    p.mass_out = static_cast<float*>(mass_out->data);
+    p.kept = static_cast<int32_t*>(kept->data);
+    p.new_lengths = static_cast<int32_t*>(new_lengths->data);
+    p.status = static_cast<int32_t*>(workspace->data);
+    p.H_kv = (int)H_kv; p.D = (int)D; p.keep = (int)keep; p.recent = (int)recent; p.mass_cells = (int)M;
+    check_cuda(kvgqa::launch_paged_evict(p, static_cast<cudaStream_t>(stream)), "paged_evict launch");
+  });
+}
+
 struct kvgqa_slots {
   kvgqa::SlotTable table;
 };

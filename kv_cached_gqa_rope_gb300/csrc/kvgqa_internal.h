@@ -129,6 +129,81 @@ cudaError_t launch_prefill_attention(const PrefillParams& p, cudaStream_t stream
 constexpr int kPrefillTile = 128;
 inline int64_t prefill_order_entries(int64_t A, int64_t T) { return A * ((T + kPrefillTile - 1) / kPrefillTile); }
 
+// ------------------------------------------------------------------ paged cache
+// Common metadata of the paged calls (see include/kvgqa.h).
+struct PagedMeta {
+  const int32_t* query_starts;  // [A + 1]: rows of the packed tokens (nullptr: no queries, the evict call)
+  const int32_t* kv_lengths;    // [A]
+  const int32_t* block_table;   // [A, max_pages]
+  int A, N, max_query_len, max_pages, max_cells, page_shift, P;
+};
+
+struct PagedStoreParams {
+  const uint16_t* q;            // [N, H_q, D], rows q_stride apart
+  const uint16_t* k;            // [N, H_kv, D]
+  const uint16_t* v;
+  const int32_t* positions;     // [axes, N]
+  uint16_t* q_out;              // [N, H_q, D]
+  uint16_t* k_cache;            // [P, H_kv, page, D]
+  uint16_t* v_cache;
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride;  // elements
+  PagedMeta m;
+  int H_q, H_kv, D, f16;
+  RopeFreqs freqs;
+  uint8_t axis[kMaxHeadDim / 2];  // the axis whose position turns each pair
+};
+cudaError_t launch_paged_rope_kv_store(const PagedStoreParams& p, cudaStream_t stream);
+
+struct PagedAttentionParams {
+  const uint16_t* q;            // [N, H_q, D] rotated
+  const uint16_t* k_cache;      // [P, H_kv, page, D]
+  const uint16_t* v_cache;
+  uint16_t* out;                // [N, H_q, D]
+  float* lse;                   // [N, H_q] or nullptr
+  int32_t* status;
+  void* cuts;                   // PagedCut per CTA (workspace)
+  float* partials;              // split results (workspace)
+  PagedMeta m;
+  int H_q, H_kv, G, D, f16, num_ctas;
+  int out_32b;                  // out is 32-byte aligned (set by the launcher)
+  int gp_shift;                 // log2 of the group size padded to a power of two (set by the launcher)
+  float scale_log2;             // scale * log2(e)
+};
+// Workspace of the paged attention behind the status block.
+struct PagedLayout {
+  int num_ctas;
+  size_t cut_bytes, partial_bytes;
+};
+cudaError_t paged_attention_layout(int device, int D, PagedLayout* out);
+cudaError_t launch_paged_attention(const PagedAttentionParams& p, cudaStream_t stream);
+
+struct PagedMassParams {
+  const uint16_t* q;            // [N, H_q, D] rotated
+  const float* lse;             // [N, H_q]
+  const uint16_t* k_cache;      // [P, H_kv, page, D]
+  float* mass;                  // [A, H_kv, mass_cells]
+  int32_t* status;
+  PagedMeta m;
+  int H_q, H_kv, G, D, f16, num_ctas, mass_cells;
+  int gp_shift, box_tokens;     // set by the launcher
+  float scale_log2;
+};
+cudaError_t launch_paged_mass(const PagedMassParams& p, cudaStream_t stream);
+
+struct PagedEvictParams {
+  const float* mass;            // [A, H_kv, mass_cells]
+  uint16_t* k_cache;            // [P, H_kv, page, D]
+  uint16_t* v_cache;
+  float* mass_out;              // [A, H_kv, mass_cells]
+  int32_t* kept;                // [A, H_kv, keep]
+  int32_t* new_lengths;         // [A]
+  int32_t* status;
+  PagedMeta m;
+  int H_kv, D, keep, recent, mass_cells;
+};
+cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
+
 // ------------------------------------------------------------------ bounded-wait check
 // One CTA whose only wait can never complete (kvgqa_check_bounded_wait).
 cudaError_t launch_bounded_wait_check(int32_t* status, cudaStream_t stream);

@@ -1,0 +1,840 @@
+// Grouped-query attention of a chunk of new tokens over a paged cache, on
+// tcgen05 tensor cores with the accumulators in tensor memory.
+//
+//   out[n, h] = sum_j softmax_j(scale * q[n, h] . k_j) v_j,  j = 0 .. the cell of token n
+//   lse[n, h] = log sum_j exp(scale * q[n, h] . k_j)
+//
+// Work.  The query heads of a KV group read the same keys, so a query tile is
+// 128 rows of (token, head of the group): 128 / GP tokens of one KV head (GP:
+// the group size padded to a power of two; the tensor map fills the padding
+// with zeros).  A segment (a, g, b) is block b of two such tiles (A and B) of
+// sequence a and KV head g; both read each 128-key tile that is staged in
+// shared memory, which is walked from cell 0 to the block's last token.  The
+// segments lie one behind the other in a virtual space of units (about one per
+// key tile, one for a segment's start and end), of which every CTA of the
+// persistent grid (one per SM) takes an equal range: long prompts, short chunks
+// and single tokens share one schedule, whose shares differ by a few units.  A
+// segment cut by a CTA boundary leaves FP32 partials (m, l, O) of the rows it
+// really has, merged by the kernel launched behind this one.
+//
+// Per key tile:
+//   warp 8      TMA of the query tiles and the K tile, one box per page (a tile
+//               takes 128 / page boxes, issued side by side by as many lanes
+//               that have each read their page's table entry);
+//   warp 9      the same for the V tile; in a sequence's last tile it zeroes the
+//               rows behind the last cell, which may hold anything (a zero
+//               weight times a NaN is a NaN);
+//   warp 10     one thread issues tcgen05.mma: S_x = Q_x K^T into TMEM and
+//               O_x += P_x V with P_x read from TMEM (x = A, B);
+//   warps 0-3   softmax of tile A, warps 4-7 of tile B, one thread per row: FP32
+//               online softmax (the base follows the row maximum only when it
+//               grew by more than 2^8; O / l stays exact), P in the storage type
+//               written back over the S columns.  P's rounding is that of the
+//               tensor cores' operand type; the sum l is of the unrounded FP32
+//               weights.
+// While one tile's softmax works on its scores, the other tile's MMAs run.
+// Long chunks are bound by the softmax's exponentials beside the MMAs, single
+// tokens by the stream of K and V.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "elem.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace kvgqa {
+namespace {
+
+constexpr int BM = 128;        // rows of a query tile
+constexpr int BN = 128;        // keys of a tile
+constexpr int ROWS = 2 * BM;   // rows of a segment's block: tiles A and B
+constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
+constexpr int THREADS = 12 * 32;
+constexpr int W_K = 8, W_V = 9, W_MMA = 10;
+// Register split (setmaxnreg): the launch gives every thread kLaunchRegs; the
+// role warpgroup drops to kRoleRegs so that the two softmax warpgroups can
+// hold a whole score row each.
+constexpr int kLaunchRegs = 168, kRoleRegs = 72, kSoftmaxRegs = 216;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kRoleRegs <= THREADS * kLaunchRegs, "register split");
+constexpr int TMEM_COLS = 512; // S_A, S_B, O_A, O_B: 128 columns each
+constexpr int UNITS_MIN = 3;   // fewest units a CTA is given
+constexpr unsigned FULLMASK = 0xffffffffu;
+
+// A segment cut at a CTA boundary, noted by the CTA where it starts.
+struct PagedCut {
+  int rows;    // rows of its block, 0: this CTA starts no cut segment
+  int tok;     // first packed token
+  int g;       // KV head
+  int last;    // last CTA that holds a part of it
+};
+// One partial result: O[ROWS][D], then m[ROWS], then l[ROWS]; slot 2b + 1 of
+// CTA b holds a segment that starts there, slot 2b one that started before.
+__host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<size_t>(ROWS) * (D + 2); }
+
+template <int D>
+struct ACfg {
+  static constexpr int NSUB = D / 64;
+  static constexpr int TILE = NSUB * SUB;           // one Q, K or V tile
+  static constexpr int NK = D == 128 ? 2 : 4;       // K stages
+  static constexpr int NV = D == 128 ? 2 : 4;       // V stages
+  static constexpr int Q_OFF = 0;                   // Q_A, Q_B
+  static constexpr int K_OFF = 2 * TILE;
+  static constexpr int V_OFF = K_OFF + NK * TILE;
+  static constexpr int STG = 32 * 128;              // output staging of one softmax warp
+  static constexpr int STG_OFF = V_OFF + NV * TILE; // (and the schedule's scratch, before any output)
+  static constexpr int BAR_OFF = STG_OFF + 8 * STG;
+  // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
+  // s_full[2], p_full[2], o_done[2], v_land, drain (index [2] = tile A / B)
+  static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 8;
+  static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int FLAG_OFF = SLOT_OFF + 8;
+  static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // + alignment slack
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// ------------------------------------------------------------------ schedule
+__device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { return ROWS >> p.gp_shift; }
+// Virtual units of a segment that ends with the block's (i - 1)-th successor
+// of token off (i = b + 1): at least its key tiles and one.
+__device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int i) {
+  return off / BN + 2 + (i * block_tokens(p) + BN - 1) / BN;
+}
+// The sum of seg_units(off, i) over i = 1 .. n, in closed form.
+__device__ __forceinline__ int sum_units(const PagedAttentionParams& p, int off, int n) {
+  int s;
+  if (p.gp_shift == 0) {
+    s = n * (n + 1);                           // 256 tokens a block: 2i
+  } else {
+    const int sh = p.gp_shift - 1, m = n >> sh, r = n & ((1 << sh) - 1);
+    s = ((m * (m + 1)) >> 1 << sh) + r * (m + 1);  // 2^sh blocks to a key tile: ceil(i / 2^sh)
+  }
+  return n * (off / BN + 2) + s;
+}
+__device__ __forceinline__ int seq_units(const PagedAttentionParams& p, const PagedSeq& s) {
+  const int tb = block_tokens(p);
+  return p.H_kv * sum_units(p, s.kl - s.ql, (s.ql + tb - 1) / tb);
+}
+
+// The range [v0, v1) of virtual units of this CTA and the sequence v0 falls
+// in, with that sequence's virtual start.  Called by the whole CTA; every CTA
+// computes the same prefix sums from the metadata.
+struct Range {
+  int v0, v1, w, a, pre;
+};
+__device__ bool find_range(const PagedAttentionParams& p, int* scratch, Range& r) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = THREADS / 32;
+  int mine = 0, bad = 0;
+  for (int a = tid; a < p.m.A; a += THREADS) {
+    const PagedSeq s = paged_seq(p.m, a);
+    bad |= !s.ok;
+    mine += seq_units(p, s);
+  }
+  if (blockIdx.x == 0 && bad) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(FULLMASK, mine, o);
+  if (lane == 0) scratch[warp] = mine;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) total += scratch[w];
+  r.w = max((total + p.num_ctas - 1) / p.num_ctas, UNITS_MIN);
+  // (num_ctas ranges of w units hold the total; a product past 2^31 would mean v0 >= total)
+  const long long v0 = static_cast<long long>(blockIdx.x) * r.w;
+  if (v0 >= total) return false;
+  r.v0 = static_cast<int>(v0);
+  r.v1 = min(r.v0 + r.w, total);
+  int carry = 0;
+  for (int base = 0; base < p.m.A; base += THREADS) {
+    const int a = base + tid;
+    const int u = a < p.m.A ? seq_units(p, paged_seq(p.m, a)) : 0;
+    int incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(FULLMASK, incl, o);
+      if (lane >= o) incl += t;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int t = scratch[w];
+      if (w < warp) before += t;
+      carry += t;
+    }
+    const int excl = before + incl - u;
+    if (u > 0 && excl <= r.v0 && r.v0 < excl + u) {
+      scratch[NW] = a;
+      scratch[NW + 1] = excl;
+    }
+  }
+  __syncthreads();
+  r.a = scratch[NW];
+  r.pre = scratch[NW + 1];
+  return true;
+}
+
+// Walks the key tiles of this CTA's range, segment by segment; every role
+// runs its own copy.
+struct PagedWalk {
+  const PagedAttentionParams* p;
+  int v0, v1;
+  int a, g, b, nblk;      // segment: sequence, KV head, block of the sequence's nblk
+  int first, ql, off;     // the sequence's first packed row, new tokens, cells before them
+  int vlo, tiles, kend;   // the segment's virtual start, key tiles, last cell + 1
+  int j, j_first, j_end;  // key tile, and this CTA's part of the segment
+  bool ok;
+
+  __device__ __forceinline__ void load_seq() {
+    const PagedSeq s = paged_seq(p->m, a);
+    first = s.first;
+    ql = s.ql;
+    off = s.kl - s.ql;
+    const int tb = block_tokens(*p);
+    nblk = (ql + tb - 1) / tb;
+  }
+  __device__ __forceinline__ bool enter() {
+    kend = off + min(ql, (b + 1) * block_tokens(*p));
+    tiles = (kend + BN - 1) / BN;
+    const int lo = max(v0, vlo), hi = min(v1, vlo + tiles);
+    j = j_first = lo - vlo;
+    j_end = hi - vlo;
+    return lo < hi;
+  }
+  __device__ bool next_segment() {
+    for (;;) {
+      vlo += seg_units(*p, off, b + 1);
+      if (vlo >= v1) return false;
+      if (++b == nblk) {
+        b = 0;
+        if (++g == p->H_kv) {
+          g = 0;
+          do {
+            if (++a >= p->m.A) return false;
+            load_seq();
+          } while (ql == 0);
+        }
+      }
+      if (enter()) return true;
+    }
+  }
+  __device__ void init(const PagedAttentionParams* params, const Range& r) {
+    p = params;
+    v0 = r.v0;
+    v1 = r.v1;
+    a = r.a;
+    load_seq();
+    int rem = v0 - r.pre;
+    const int head = sum_units(*p, off, nblk);
+    g = rem / head;
+    rem -= g * head;
+    int lo = 0, hi = nblk - 1;  // the block whose units hold v0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sum_units(*p, off, mid) <= rem) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+    vlo = v0 - rem + sum_units(*p, off, b);
+    ok = enter() || next_segment();
+  }
+  __device__ __forceinline__ bool fresh() const { return j == j_first; }
+  __device__ __forceinline__ bool last() const { return j == j_end - 1; }
+  // Whether the block has rows in tile B.
+  __device__ __forceinline__ bool dual() const { return (ql - b * block_tokens(*p)) << p->gp_shift > BM; }
+  __device__ __forceinline__ bool whole() const { return vlo >= v0 && vlo + tiles <= v1; }
+  __device__ __forceinline__ int tok0() const { return b * block_tokens(*p); }
+  __device__ __forceinline__ void advance() {
+    if (j < j_end - 1) ++j;
+    else ok = next_segment();
+  }
+};
+
+// The TMA boxes of the walk's K or V tile: lane i < boxes() takes the cells
+// from j * BN + i * box_rows on.
+struct TileBoxes {
+  int n, rows, c1, c2;  // boxes of the tile; cells of a box; this lane's coordinates
+};
+__device__ __forceinline__ TileBoxes tile_boxes(const PagedWalk& w, int lane) {
+  const PagedAttentionParams& p = *w.p;
+  TileBoxes t;
+  t.rows = min(1 << p.m.page_shift, BN);
+  t.n = (min(BN, w.kend - w.j * BN) + t.rows - 1) / t.rows;
+  t.c1 = t.c2 = 0;
+  if (lane < t.n) {
+    const int cell = w.j * BN + lane * t.rows;
+    const int pid = paged_page(p.m, w.a, cell);
+    if (pid < 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
+    t.c1 = cell & ((1 << p.m.page_shift) - 1);
+    t.c2 = pid < 0 ? -1 : pid * p.H_kv + w.g;  // outside the map: zeros
+  }
+  return t;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(THREADS, 1)
+paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const __grid_constant__ CUtensorMap map_o) {
+  using C = ACfg<D>;
+  using E = Elem<F16>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* q_full = bars;       // [tile]
+  uint64_t* q_empty = bars + 2;  // [tile]
+  uint64_t* k_full = bars + 4;
+  uint64_t* k_empty = k_full + C::NK;
+  uint64_t* v_full = k_empty + C::NK;
+  uint64_t* v_empty = v_full + C::NV;
+  uint64_t* s_full = v_empty + C::NV;  // [tile]
+  uint64_t* p_full = s_full + 2;       // [tile]
+  uint64_t* o_done = p_full + 2;       // [tile]
+  uint64_t* v_land = o_done + 2;       // a sequence's last V tile has landed
+  uint64_t* drain = v_land + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PagedCut* cut = static_cast<PagedCut*>(p.cuts) + blockIdx.x;
+
+  pdl_wait();
+  if (threadIdx.x == 0) cut->rows = 0;
+  Range range;
+  if (!find_range(p, reinterpret_cast<int*>(smem + C::STG_OFF), range)) return;  // uniform
+  PagedWalk walk;
+  walk.init(&p, range);
+  if (!walk.ok) return;  // uniform: nothing but padding in this range
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);  // one arrival per softmax warp
+      mbar_init(&o_done[x], 1);
+    }
+    mbar_init(v_land, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+
+  if (warp >= 8) {
+  regs_dec<kRoleRegs>();
+  // Whether every lane's wait succeeded (a timeout anywhere stops the warp).
+#define KVGQA_WAIT(bar, parity) __all_sync(FULLMASK, mbar_wait_bounded((bar), (parity), abort_flag, p.status))
+  if (warp == W_K) {
+    // ------------------------------------------------------------ Q and K producer
+    const uint64_t pol_q = l2_evict_first_policy();
+    const uint64_t pol_kv = l2_evict_last_policy();  // re-read by the sequence's other blocks
+    int it = 0, qn[2] = {0, 0};  // K tiles, and Q tiles (A, B) loaded so far
+    auto load_q = [&](int x) -> bool {
+      if (qn[x] >= 1 && !KVGQA_WAIT(&q_empty[x], (qn[x] - 1) & 1)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full[x], BM * D * 2);
+        for (int sub = 0; sub < C::NSUB; ++sub)
+          tma_load_4d(smem + C::Q_OFF + x * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g,
+                      walk.first + walk.tok0() + x * (BM >> p.gp_shift), &q_full[x], pol_q);
+      }
+      ++qn[x];
+      return true;
+    };
+    for (; walk.ok; walk.advance()) {
+      const bool fresh = walk.fresh();
+      if (fresh && !load_q(0)) break;
+      const int s = it % C::NK;
+      const TileBoxes t = tile_boxes(walk, lane);
+      if (it >= C::NK && !KVGQA_WAIT(&k_empty[s], ((it / C::NK) - 1) & 1)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[s], t.n * t.rows * 128 * C::NSUB);
+      __syncwarp();
+      if (lane < t.n) {
+        unsigned char* st = smem + C::K_OFF + s * C::TILE + lane * t.rows * 128;
+        for (int sub = 0; sub < C::NSUB; ++sub)
+          tma_load_3d(st + sub * SUB, &map_k, sub * 64, t.c1, t.c2, &k_full[s], pol_kv);
+      }
+      ++it;
+      if (fresh && walk.dual() && !load_q(1)) break;
+    }
+    __syncwarp();
+    if (*abort_flag) {  // let the copies in flight land
+      volatile int none = 0;
+      for (int x = 0; x < 2; ++x)
+        if (qn[x] >= 1) mbar_wait_bounded(&q_full[x], (qn[x] - 1) & 1, &none, nullptr);
+      for (int t = it - C::NK < 0 ? 0 : it - C::NK; t < it; ++t)
+        mbar_wait_bounded(&k_full[t % C::NK], (t / C::NK) & 1, &none, nullptr);
+    }
+  } else if (warp == W_V) {
+    // ------------------------------------------------------------ V producer
+    const uint64_t pol_kv = l2_evict_last_policy();
+    int it = 0, landed = 0;
+    for (; walk.ok; walk.advance()) {
+      const int s = it % C::NV;
+      const TileBoxes t = tile_boxes(walk, lane);
+      if (it >= C::NV && !KVGQA_WAIT(&v_empty[s], ((it / C::NV) - 1) & 1)) break;
+      const int live = walk.kend - walk.j * BN;  // cells of this tile
+      uint64_t* bar = live < BN ? v_land : &v_full[s];
+      unsigned char* st = smem + C::V_OFF + s * C::TILE;
+      if (lane == 0) mbar_arrive_expect_tx(bar, t.n * t.rows * 128 * C::NSUB);
+      __syncwarp();
+      if (lane < t.n)
+        for (int sub = 0; sub < C::NSUB; ++sub)
+          tma_load_3d(st + sub * SUB + lane * t.rows * 128, &map_v, sub * 64, t.c1, t.c2, bar, pol_kv);
+      ++it;
+      if (live < BN) {
+        // the cells behind the last one weigh zero, and must not be NaN
+        if (!KVGQA_WAIT(v_land, landed & 1)) break;
+        ++landed;
+        for (int i = live * 8 + lane; i < BN * 8; i += 32)
+#pragma unroll
+          for (int sub = 0; sub < C::NSUB; ++sub)
+            *reinterpret_cast<uint4*>(st + sub * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_full[s]);
+      }
+    }
+    __syncwarp();
+    if (*abort_flag) {
+      volatile int none = 0;
+      mbar_wait_bounded(v_land, landed & 1, &none, nullptr);
+      for (int t = it - C::NV < 0 ? 0 : it - C::NV; t < it; ++t)
+        mbar_wait_bounded(&v_full[t % C::NV], (t / C::NV) & 1, &none, nullptr);
+    }
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop; one elected lane issues each group of
+    // MMAs and its commits.  Step t: P.V of tile t, then S of tile t + 1, for
+    // A, then for B (where the tile's segment has rows in B).
+    constexpr uint32_t IDESC_QK = idesc_f16kind_f32(E::kMmaFormat, BM, BN, 0);
+    constexpr uint32_t IDESC_PV = idesc_f16kind_f32(E::kMmaFormat, BM, D, 1);
+    bool issued = false, ok = true;
+    int qn = 0, qnb = 0;         // Q tiles A and B consumed
+    int pn = 0, pnb = 0;         // P tiles A and B consumed
+    bool first = false, dual = false;  // of tile t
+    for (int t = -1; ok; ++t) {
+      const bool more = walk.ok;
+      const int sv = t % C::NV, kn = (t + 1) % C::NK;
+      if (t >= 0) ok = KVGQA_WAIT(&v_full[sv], (t / C::NV) & 1);
+      if (ok && more) ok = KVGQA_WAIT(&k_full[kn], ((t + 1) / C::NK) & 1);
+      if (!ok) break;
+      const uint32_t v_addr = sbase + C::V_OFF + sv * C::TILE;
+      const uint32_t k_addr = sbase + C::K_OFF + kn * C::TILE;
+      const bool n_first = more && walk.fresh(), n_last = more && walk.last(), n_dual = more && walk.dual();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (t >= 0 && (x == 0 || dual)) {
+          int& n = x == 0 ? pn : pnb;
+          ok = KVGQA_WAIT(&p_full[x], n & 1);
+          if (!ok) break;
+          ++n;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+              umma_f16_ts(tmem + (2 + x) * BN, tmem + x * BN + ks * 8, smem_desc_sw128(v_addr + ks * 2048, SUB, 1024),
+                          IDESC_PV, (ks > 0 || !first) ? 1u : 0u);
+            umma_commit(&o_done[x]);
+            if (x == 1 || !dual) umma_commit(&v_empty[sv]);
+          }
+          __syncwarp();
+        }
+        if (more && (x == 0 || n_dual)) {
+          if (n_first) {
+            int& n = x == 0 ? qn : qnb;
+            ok = KVGQA_WAIT(&q_full[x], n & 1);
+            if (!ok) break;
+            ++n;
+          }
+          tc_fence_after();
+          const uint32_t q_addr = sbase + C::Q_OFF + x * C::TILE;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t o = (ks / 4) * SUB + (ks % 4) * 32;
+              umma_f16_ss(tmem + x * BN, smem_desc_sw128(q_addr + o, 16, 1024), smem_desc_sw128(k_addr + o, 16, 1024),
+                          IDESC_QK, ks > 0);
+            }
+            umma_commit(&s_full[x]);
+            if (n_last) umma_commit(&q_empty[x]);
+            if (x == 1 || !n_dual) umma_commit(&k_empty[kn]);
+          }
+          __syncwarp();
+          issued = true;
+        }
+      }
+      if (!more) break;
+      first = n_first;
+      dual = n_dual;
+      walk.advance();
+    }
+    if (*abort_flag && issued) {
+      // let every MMA issued so far finish before TMEM is released
+      if (elect_one()) umma_commit(drain);
+      __syncwarp();
+      volatile int none = 0;
+      mbar_wait_bounded(drain, 0, &none, nullptr);
+    }
+  }
+#undef KVGQA_WAIT
+  } else {
+    // ------------------------------------------------------------ softmax (warps 0-7)
+    regs_inc<kSoftmaxRegs>();
+    const int x = warp >> 2;           // tile A or B
+    const int r = threadIdx.x & 127;   // row of the tile == TMEM lane
+    const int row_tok = (x * BM + r) >> p.gp_shift;  // token of the row, within the block
+    const int row_g = r & ((1 << p.gp_shift) - 1);   // head of the group
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + x * BN;
+    const uint32_t o_col = tmem + lane_base + (2 + x) * BN;
+    const float c = p.scale_log2;
+    const float ce = c > 0.f ? c : 1.f;
+    float m_ref = -INFINITY, l = 0.f;
+    int t = 0;  // tiles of this group so far
+    for (; walk.ok; walk.advance()) {
+      if (x == 1 && !walk.dual()) continue;  // no rows in tile B
+      const bool first = walk.fresh(), last = walk.last();
+      // Row r sees column i of the tile iff i <= thr.
+      const int thr0 = walk.off + walk.tok0() - walk.j * BN;
+      const int thr = thr0 + row_tok;
+      if (!__all_sync(FULLMASK, mbar_wait_bounded(&s_full[x], t & 1, abort_flag, p.status))) break;
+      tc_fence_after();
+      // Scores enter the softmax as s * ce with ce > 0 (a scale that is not
+      // positive is folded into the scores first).
+      uint32_t u[BN];
+#pragma unroll
+      for (int q = 0; q < BN / 32; ++q) tmem_ld32(s_col + q * 32, *reinterpret_cast<uint32_t(*)[32]>(u + q * 32));
+      tmem_wait_ld();
+      float* sv = reinterpret_cast<float*>(u);
+      if (c <= 0.f) {
+#pragma unroll
+        for (int i = 0; i < BN; ++i) sv[i] *= c;
+      }
+      if (thr0 + ((x * BM) >> p.gp_shift) < BN - 1) {  // a tile that reaches past a row's cell
+#pragma unroll
+        for (int i = 0; i < BN; ++i) sv[i] = i <= thr ? sv[i] : -INFINITY;
+      }
+      float mx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx[k] = fmaxf(sv[2 * k], sv[2 * k + 1]);
+#pragma unroll
+      for (int i = 16; i < BN; i += 16) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = fmax3(mx[k], sv[i + 2 * k], sv[i + 2 * k + 1]);
+      }
+      const float mraw = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+      const float mt = mraw * ce;                    // tile maximum of the scaled scores
+      const bool grow = first || mt > m_ref + 8.f;   // keep the old base unless it grew by 2^8
+      float alpha = 1.f;
+      if (grow) {
+        alpha = first ? 0.f : ex2(m_ref - mt);
+        m_ref = mt;
+        l = first ? 0.f : l * alpha;  // (the last segment's row may have been padding, its sum anything)
+      }
+      // S_x of this tile being ready means the P.V of the previous tile is
+      // complete, so O_x may be rescaled here without a further wait.
+      if (__any_sync(FULLMASK, grow && !first)) {
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t w[32];
+          tmem_ld32(o_col + q * 32, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+          tmem_st32(o_col + q * 32, w);
+        }
+      }
+      // A row that has seen no cell yet (the part of a cut segment may begin
+      // in tiles that only later tokens see) keeps the base -inf; its weights
+      // are 2^(-inf - 0) = 0.
+      const float base = m_ref == -INFINITY ? 0.f : -m_ref;
+      float2 ls = make_float2(0.f, 0.f);
+      const float2 c2 = make_float2(ce, ce), nm2 = make_float2(base, base);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int i0 = half * 64 + 2 * e;
+          const float2 xx = ffma2(make_float2(sv[i0], sv[i0 + 1]), c2, nm2);
+          const float2 pr = make_float2(ex2(xx.x), ex2(xx.y));
+          ls = fadd2(ls, pr);
+          w[e] = E::pack2(pr.x, pr.y);
+        }
+        tmem_st32(s_col + half * 32, w);
+      }
+      tmem_wait_st();
+      l += ls.x + ls.y;
+      // Each warp arrives once: every lane's TMEM stores are complete and
+      // fenced before the warp synchronises, then lane 0 arrives.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[x]);
+
+      if (last) {
+        // ---------------------------------------------------- end of this part of the segment
+        if (!__all_sync(FULLMASK, mbar_wait_bounded(&o_done[x], t & 1, abort_flag, p.status))) break;
+        tc_fence_after();
+        const int tok = walk.tok0() + row_tok;
+        const bool row_ok = tok < walk.ql && row_g < p.G;
+        if (walk.whole()) {
+          const float inv = 1.f / l;
+          const size_t head = static_cast<size_t>(walk.first + tok) * p.H_q + walk.g * p.G + row_g;
+          // This warp's 32 rows go out through shared memory and a TMA store
+          // when all of its tokens belong to the sequence; else the rows that
+          // do take direct stores.
+          const int warp_tok = (x * BM + (warp & 3) * 32) >> p.gp_shift;
+          const bool via_tma = walk.tok0() + warp_tok + (32 >> p.gp_shift) <= walk.ql;
+          unsigned char* stg = smem + C::STG_OFF + warp * C::STG;
+          uint16_t* dst = p.out + head * D;
+          if (row_ok && p.lse) p.lse[head] = (m_ref + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+          for (int sub = 0; sub < C::NSUB; ++sub) {  // 64 output values of the row at a time
+            uint32_t v[64];
+            tmem_ld32(o_col + sub * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld32(o_col + sub * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            tmem_wait_ld();
+            uint32_t w[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              w[k] = E::pack2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+            if (via_tma) {
+              if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // 16-byte chunk k of row `lane` at its 128B-swizzled place
+                *reinterpret_cast<uint4*>(stg + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                    make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_4d(&map_o, stg, sub * 64, 0, walk.g, walk.first + walk.tok0() + warp_tok);
+                bulk_commit_group();
+              }
+            } else if (row_ok) {
+#pragma unroll
+              for (int q16 = 0; q16 < 4; ++q16) {  // 16 values: a whole 32-byte sector
+                uint16_t* o = dst + sub * 64 + q16 * 16;
+                const uint32_t(&w8)[8] = *reinterpret_cast<const uint32_t(*)[8]>(w + 8 * q16);
+                if (p.out_32b) {
+                  stg256_stream(o, w8);
+                } else {
+                  *reinterpret_cast<uint4*>(o) = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                  *reinterpret_cast<uint4*>(o + 8) = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+                }
+              }
+            }
+          }
+        } else {
+          const bool starts = walk.vlo >= walk.v0;
+          float* slot = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + starts) * slot_floats(D);
+          const int row = x * BM + r;
+          if (starts && threadIdx.x == 0) {
+            cut->tok = walk.first + walk.tok0();
+            cut->g = walk.g;
+            cut->last = (walk.vlo + walk.tiles - 1) / range.w;
+            cut->rows = min(ROWS, (walk.ql - walk.tok0()) << p.gp_shift);
+          }
+          if (row_ok) {
+            slot[ROWS * D + row] = m_ref;
+            slot[ROWS * D + ROWS + row] = l;
+          }
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(o_col + q * 32, v);
+            tmem_wait_ld();
+            if (row_ok) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(slot + row * D + q * 32 + k * 4) =
+                    make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+        }
+      }
+      ++t;
+    }
+  }
+
+  if (warp < 8 && lane == 0) bulk_wait_group<0>();  // this warp's output stores are complete
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+// ------------------------------------------------------------------ merge of cut segments
+// CTA (b, y): row group y of the cut segment that starts in CTA b of the
+// attention kernel, one warp per row.  A part whose maximum is -inf saw none
+// of the row's cells and weighs nothing.
+constexpr int kMergeWarps = 8, kMergeGroups = 8;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttentionParams p) {
+  constexpr int VL = D / 32;  // values per lane
+  using E = Elem<F16>;
+  pdl_wait();
+  const int b0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedCut cut = static_cast<const PagedCut*>(p.cuts)[b0];
+  for (int row = blockIdx.y * kMergeWarps + warp; row < cut.rows; row += kMergeGroups * kMergeWarps) {
+    const int gi = row & ((1 << p.gp_shift) - 1);
+    if (gi >= p.G) continue;
+    auto part = [&](int b) { return p.partials + (static_cast<size_t>(b) * 2 + (b == b0)) * slot_floats(D); };
+    float M = -INFINITY;
+    for (int b = b0 + lane; b <= cut.last; b += 32) M = fmaxf(M, part(b)[ROWS * D + row]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULLMASK, M, o));
+    float l = 0.f, acc[VL] = {};
+#pragma unroll 4
+    for (int b = b0; b <= cut.last; ++b) {
+      const float* s = part(b);
+      const float m = s[ROWS * D + row], lb = s[ROWS * D + ROWS + row];
+      float o[VL];
+      if constexpr (VL == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(s + row * D + lane * 4);
+      else *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(s + row * D + lane * 2);
+      if (m == -INFINITY) continue;
+      const float w = exp2f(m - M);
+      l += w * lb;
+#pragma unroll
+      for (int k = 0; k < VL; ++k) acc[k] += w * o[k];
+    }
+    const float inv = 1.f / l;
+    const size_t head = static_cast<size_t>(cut.tok + (row >> p.gp_shift)) * p.H_q + cut.g * p.G + gi;
+    uint32_t w[VL / 2];
+#pragma unroll
+    for (int k = 0; k < VL / 2; ++k) w[k] = E::pack2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    uint16_t* dst = p.out + head * D + lane * VL;
+    if constexpr (VL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+struct Maps {
+  CUtensorMap q, k, v, o;
+};
+
+cudaError_t make_maps(const PagedAttentionParams& p, Maps* m) {
+  auto enc = tma_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const CUtensorMapDataType type = p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t D = p.D, G = p.G, Hkv = p.H_kv;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const cuuint32_t gp = 1u << p.gp_shift;
+  for (int t = 0; t < 2; ++t) {  // q, and out in boxes of 32 rows
+    const cuuint64_t dims[4] = {D, G, Hkv, static_cast<cuuint64_t>(p.m.N)};
+    const cuuint64_t strides[3] = {D * 2, D * 2 * G, D * 2 * G * Hkv};
+    const cuuint32_t box[4] = {64, gp, 1, (t == 0 ? BM : 32) / gp};
+    if (enc(t == 0 ? &m->q : &m->o, type, 4, t == 0 ? const_cast<uint16_t*>(p.q) : p.out, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  const cuuint64_t page = 1ull << p.m.page_shift;
+  for (int t = 0; t < 2; ++t) {
+    const cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(p.m.P) * Hkv};
+    const cuuint64_t strides[2] = {D * 2, D * 2 * page};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page < BN ? page : BN), 1};
+    if (enc(t == 0 ? &m->k : &m->v, type, 3, const_cast<uint16_t*>(t == 0 ? p.k_cache : p.v_cache), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
+template <int D, bool F16>
+cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t stream) {
+  static std::once_flag flags[64];
+  static cudaError_t errs[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(flags[dev], [&] {
+    errs[dev] = cudaFuncSetAttribute(paged_attention_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     ACfg<D>::SMEM);
+    // setmaxnreg.inc is only satisfied if the launch hands out kLaunchRegs per thread.
+    cudaFuncAttributes attr;
+    if (errs[dev] == cudaSuccess) errs[dev] = cudaFuncGetAttributes(&attr, paged_attention_kernel<D, F16>);
+    if (errs[dev] == cudaSuccess && attr.numRegs < kLaunchRegs) errs[dev] = cudaErrorInvalidConfiguration;
+  });
+  if (errs[dev] != cudaSuccess) return errs[dev];
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = ACfg<D>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, F16>, p, m.q, m.k, m.v, m.o);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(p.num_ctas, kMergeGroups);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F16>, p);
+}
+
+}  // namespace
+
+cudaError_t paged_attention_layout(int device, int D, PagedLayout* out) {
+  static int sms[64];
+  static std::once_flag flags[64];
+  static cudaError_t errs[64];
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  std::call_once(flags[device], [&] {
+    errs[device] = cudaDeviceGetAttribute(&sms[device], cudaDevAttrMultiProcessorCount, device);
+  });
+  if (errs[device] != cudaSuccess) return errs[device];
+  out->num_ctas = sms[device];
+  out->cut_bytes = (sms[device] * sizeof(PagedCut) + 255) / 256 * 256;
+  out->partial_bytes = static_cast<size_t>(sms[device]) * 2 * slot_floats(D) * sizeof(float);
+  return cudaSuccess;
+}
+
+cudaError_t launch_paged_attention(const PagedAttentionParams& params, cudaStream_t stream) {
+  if (params.m.A == 0 || params.m.N == 0) return cudaSuccess;
+  PagedAttentionParams p = params;
+  p.out_32b = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+  p.gp_shift = 0;
+  while ((1 << p.gp_shift) < p.G) ++p.gp_shift;
+  Maps m;
+  const cudaError_t e = make_maps(p, &m);
+  if (e != cudaSuccess) return e;
+  if (p.D == 128) return p.f16 ? launch_d<128, true>(p, m, stream) : launch_d<128, false>(p, m, stream);
+  if (p.D == 64) return p.f16 ? launch_d<64, true>(p, m, stream) : launch_d<64, false>(p, m, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvgqa

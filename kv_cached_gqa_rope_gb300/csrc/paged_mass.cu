@@ -1,0 +1,536 @@
+// The attention weight that each cell of a paged cache gets from a chunk of
+// new tokens, added to what it has so far:
+//
+//   mass[a, g, j] += sum over tokens n of sequence a that see cell j, heads h of KV head g,
+//                    of exp(scale * q[n, h] . k_j - lse[n, h])
+//
+// lse comes with the attention's output, so the weights need K alone: no
+// softmax state, no V.  A cell's sum is over queries, so the scores are laid
+// out transposed, S^T = K Q^T with one TMEM lane per cell: each thread adds up
+// one cell's weights in registers, and nothing crosses threads until it writes
+// its cell.  Every cell is summed by one thread in one order (no atomics), so
+// the result does not depend on how the work is dealt.
+//
+// An item is 256 cells of one sequence and KV head (two 128-cell tiles, A and
+// B).  The queries of the KV group are its columns, (token, head of the group)
+// with the group padded to a power of two, in blocks of 128.  Per item:
+//   warp 8      TMA of the two K tiles, one box per page (2-stage ring);
+//   warp 9      TMA of the query blocks (ring) and their log sums, as base-2
+//               logs, into shared memory (+inf for columns without a query);
+//   warp 10     S_x^T = K_x Q^T of each block into TMEM (x = A, B, two buffers each);
+//   warps 0-3   tile A, warps 4-7 tile B: exp2 of the scaled scores less the
+//               column's log sum, added to the cell's sum; at the item's end
+//               each thread updates its cell.
+// The items are dealt as contiguous equal shares of their column blocks to a
+// persistent grid.  Single tokens are bound by the stream of K, longer chunks
+// by the exponentials.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "elem.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace kvgqa {
+namespace {
+
+constexpr int BK = 128;        // cells of a tile (= MMA M = TMEM lanes)
+constexpr int ITEM = 2 * BK;   // cells of an item
+constexpr int BC = 128;        // columns of a block
+constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
+constexpr int THREADS = 11 * 32;
+constexpr int W_K = 8, W_Q = 9, W_MMA = 10;
+constexpr int TMEM_COLS = 512; // S^T of A and B, two buffers each, 128 columns
+constexpr int NL = 8;          // log-sum slots
+constexpr unsigned FULLMASK = 0xffffffffu;
+
+template <int D>
+struct MCfg {
+  static constexpr int NSUB = D / 64;
+  static constexpr int TILE = NSUB * SUB;
+  static constexpr int NK = D == 128 ? 2 : 4;       // items in flight
+  static constexpr int NQ = 2;                      // query blocks in flight
+  static constexpr int K_OFF = 0;
+  static constexpr int Q_OFF = NK * 2 * TILE;
+  static constexpr int LSE_OFF = Q_OFF + NQ * TILE;
+  static constexpr int SCR_OFF = LSE_OFF + NL * BC * 4;
+  // k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL], s_full[4], s_empty[4], drain
+  static constexpr int BAR_OFF = SCR_OFF + 64 * 4;
+  static constexpr int NBAR = 2 * NK + 2 * NQ + 2 * NL + 9;
+  static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
+  static constexpr int FLAG_OFF = SLOT_OFF + 8;
+  static constexpr int SMEM = FLAG_OFF + 16 + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// Column blocks of a sequence, and the units of its items: one per column
+// block and tile pair, one for the item itself.
+__device__ __forceinline__ int col_blocks(const PagedMassParams& p, const PagedSeq& s) {
+  return ((s.ql << p.gp_shift) + BC - 1) / BC;
+}
+__device__ __forceinline__ int item_units(const PagedMassParams& p, const PagedSeq& s) {
+  return s.ql > 0 ? col_blocks(p, s) + 1 : 0;
+}
+__device__ __forceinline__ int seq_units(const PagedMassParams& p, const PagedSeq& s) {
+  return p.H_kv * ((s.kl + ITEM - 1) / ITEM) * item_units(p, s);
+}
+
+// Walks the items whose first unit lies in this CTA's range.
+struct MassWalk {
+  const PagedMassParams* p;
+  int v, v1;              // the item's first unit, the end of the range
+  int a, g, kb;           // sequence, KV head, item of the head
+  int first, ql, kl, off, n_items, units, nblk;
+  bool ok;
+
+  __device__ __forceinline__ void load_seq() {
+    const PagedSeq s = paged_seq(p->m, a);
+    first = s.first;
+    ql = s.ql;
+    kl = s.kl;
+    off = kl - ql;
+    n_items = (kl + ITEM - 1) / ITEM;
+    units = item_units(*p, s);
+    nblk = col_blocks(*p, s);
+  }
+  __device__ void advance() {
+    v += units;
+    if (++kb == n_items) {
+      kb = 0;
+      if (++g == p->H_kv) {
+        g = 0;
+        do {
+          if (++a >= p->m.A) {
+            ok = false;
+            return;
+          }
+          load_seq();
+        } while (ql == 0);
+      }
+    }
+    ok = v < v1;
+  }
+  // pre: the first unit of sequence `seq`, which v0 falls in.
+  __device__ void init(const PagedMassParams* params, int seq, int pre, int v0, int end) {
+    p = params;
+    v1 = end;
+    a = seq;
+    load_seq();
+    const int i = (v0 - pre + units - 1) / units;  // the first item from v0 on
+    v = pre + i * units;
+    g = i / n_items;
+    kb = i % n_items;
+    ok = v < v1;
+    if (g == p->H_kv) {  // it is the next sequence's
+      g = p->H_kv - 1;
+      kb = n_items - 1;
+      v -= units;
+      advance();
+    }
+  }
+  // Cells of tile x of the item.
+  __device__ __forceinline__ int live(int x) const { return min(BK, kl - kb * ITEM - x * BK); }
+  __device__ __forceinline__ int tiles() const { return live(1) > 0 ? 2 : 1; }
+  // The first column block of which some token sees a cell of tile x (the
+  // last token sees every cell, so the last block always counts).
+  __device__ __forceinline__ int first_block(int x) const {
+    const int t = kb * ITEM + x * BK - off;  // the first token that sees the tile
+    return t <= 0 ? 0 : (t << p->gp_shift) / BC;
+  }
+};
+
+// This CTA's range of units and the sequence it begins in; false if there is
+// none.  Every CTA computes the same prefix sums from the metadata.
+__device__ bool find_start(const PagedMassParams& p, int* scratch, int& a0, int& pre, int& v0, int& v1) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NW = THREADS / 32;
+  int mine = 0, bad = 0;
+  for (int a = tid; a < p.m.A; a += THREADS) {
+    const PagedSeq s = paged_seq(p.m, a);
+    bad |= !s.ok;
+    mine += seq_units(p, s);
+  }
+  if (blockIdx.x == 0 && bad) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(FULLMASK, mine, o);
+  if (lane == 0) scratch[warp] = mine;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) total += scratch[w];
+  const int w = max((total + p.num_ctas - 1) / p.num_ctas, 1);
+  const long long start = static_cast<long long>(blockIdx.x) * w;
+  if (start >= total) return false;
+  v0 = static_cast<int>(start);
+  v1 = min(v0 + w, total);
+  int carry = 0;
+  for (int base = 0; base < p.m.A; base += THREADS) {
+    const int a = base + tid;
+    const int u = a < p.m.A ? seq_units(p, paged_seq(p.m, a)) : 0;
+    int incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(FULLMASK, incl, o);
+      if (lane >= o) incl += t;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int t = scratch[i];
+      if (i < warp) before += t;
+      carry += t;
+    }
+    const int excl = before + incl - u;
+    if (u > 0 && excl <= v0 && v0 < excl + u) {
+      scratch[NW] = a;
+      scratch[NW + 1] = excl;
+    }
+  }
+  __syncthreads();
+  a0 = scratch[NW];
+  pre = scratch[NW + 1];
+  return true;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(THREADS, 1)
+paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_constant__ CUtensorMap map_q,
+                  const __grid_constant__ CUtensorMap map_k) {
+  using C = MCfg<D>;
+  using E = Elem<F16>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* k_empty = k_full + C::NK;
+  uint64_t* q_full = k_empty + C::NK;
+  uint64_t* q_empty = q_full + C::NQ;
+  uint64_t* l_full = q_empty + C::NQ;
+  uint64_t* l_empty = l_full + NL;
+  uint64_t* s_full = l_empty + NL;    // [tile * 2 + buffer]
+  uint64_t* s_empty = s_full + 4;
+  uint64_t* drain = s_empty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
+  float* lse_s = reinterpret_cast<float*>(smem + C::LSE_OFF);  // [NL][BC]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_wait();
+  int a0 = 0, pre = 0, v0 = 0, v1 = 0;
+  if (!find_start(p, reinterpret_cast<int*>(smem + C::SCR_OFF), a0, pre, v0, v1)) return;  // uniform
+  MassWalk walk;
+  walk.init(&p, a0, pre, v0, v1);
+  if (!walk.ok) return;  // uniform: no item begins in this range
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < C::NQ; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < NL; ++s) {
+      mbar_init(&l_full[s], 1);
+      mbar_init(&l_empty[s], 8);  // every softmax warp, whether its tile uses the block or not
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_empty[s], 4);  // one arrival per warp of the tile's group
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == W_MMA) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+#define KVGQA_WAIT(bar, parity) __all_sync(FULLMASK, mbar_wait_bounded((bar), (parity), abort_flag, p.status))
+
+  if (warp == W_K) {
+    // ------------------------------------------------------------ K producer
+    const uint64_t pol = l2_evict_first_policy();  // each cell is read once
+    const int rows = min(1 << p.m.page_shift, BK);
+    int it = 0;
+    for (; walk.ok; walk.advance(), ++it) {
+      const int s = it % C::NK;
+      // box i of the item holds the cells kb * ITEM + i * rows ..; at most 16
+      const int n = (min(ITEM, walk.kl - walk.kb * ITEM) + rows - 1) / rows;
+      int c1 = 0, c2 = 0;
+      if (lane < n) {
+        const int cell = walk.kb * ITEM + lane * rows;
+        const int pid = paged_page(p.m, walk.a, cell);
+        if (pid < 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
+        c1 = cell & ((1 << p.m.page_shift) - 1);
+        c2 = pid < 0 ? -1 : pid * p.H_kv + walk.g;  // outside the map: zeros
+      }
+      if (it >= C::NK && !KVGQA_WAIT(&k_empty[s], ((it / C::NK) - 1) & 1)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[s], n * rows * 128 * C::NSUB);
+      __syncwarp();
+      if (lane < n) {
+        const int r = lane * rows;
+        unsigned char* st = smem + C::K_OFF + (s * 2 + r / BK) * C::TILE + r % BK * 128;
+        for (int sub = 0; sub < C::NSUB; ++sub)
+          tma_load_3d(st + sub * SUB, &map_k, sub * 64, c1, c2, &k_full[s], pol);
+      }
+    }
+    __syncwarp();
+    if (*abort_flag) {
+      volatile int none = 0;
+      for (int t = it - C::NK < 0 ? 0 : it - C::NK; t < it; ++t)
+        mbar_wait_bounded(&k_full[t % C::NK], (t / C::NK) & 1, &none, nullptr);
+    }
+  } else if (warp == W_Q) {
+    // ------------------------------------------------------------ queries and log sums
+    const uint64_t pol = l2_evict_last_policy();
+    const int gp = 1 << p.gp_shift;
+    int n = 0;  // blocks so far
+    bool ok = true;
+    for (; walk.ok && ok; walk.advance()) {
+      for (int blk = walk.first_block(0); blk < walk.nblk; ++blk, ++n) {
+        const int tok0 = (blk * BC) >> p.gp_shift;
+        // log sums of this lane's 4 columns, in base 2 (loaded before the wait)
+        float ls[BC / 32];
+#pragma unroll
+        for (int i = 0; i < BC / 32; ++i) {
+          const int col = lane + 32 * i, t = tok0 + (col >> p.gp_shift), h = col & (gp - 1);
+          ls[i] = INFINITY;
+          if (t < walk.ql && h < p.G)
+            ls[i] = p.lse[static_cast<size_t>(walk.first + t) * p.H_q + walk.g * p.G + h] * 1.4426950408889634f;
+        }
+        const int s = n % C::NQ;
+        ok = (n < C::NQ || KVGQA_WAIT(&q_empty[s], ((n / C::NQ) - 1) & 1)) &&
+             (n < NL || KVGQA_WAIT(&l_empty[n % NL], ((n / NL) - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[s], p.box_tokens * gp * 128 * C::NSUB);
+          for (int sub = 0; sub < C::NSUB; ++sub)
+            tma_load_4d(smem + C::Q_OFF + s * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g, walk.first + tok0,
+                        &q_full[s], pol);
+        }
+#pragma unroll
+        for (int i = 0; i < BC / 32; ++i) lse_s[(n % NL) * BC + lane + 32 * i] = ls[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_full[n % NL]);
+      }
+    }
+    __syncwarp();
+    if (*abort_flag) {
+      volatile int none = 0;
+      for (int t = n - C::NQ < 0 ? 0 : n - C::NQ; t < n; ++t)
+        mbar_wait_bounded(&q_full[t % C::NQ], (t / C::NQ) & 1, &none, nullptr);
+    }
+  } else if (warp == W_MMA) {
+    // ------------------------------------------------------------ MMA issuer
+    int it = 0, n = 0, sn[2] = {0, 0};
+    bool ok = true, issued = false;
+    for (; walk.ok && ok; walk.advance(), ++it) {
+      const int ks = it % C::NK;
+      if (!KVGQA_WAIT(&k_full[ks], (it / C::NK) & 1)) break;
+      const int fb0 = walk.first_block(0), fb1 = walk.first_block(1), tiles = walk.tiles();
+      for (int blk = fb0; blk < walk.nblk; ++blk, ++n) {
+        const int qs = n % C::NQ;
+        ok = KVGQA_WAIT(&q_full[qs], (n / C::NQ) & 1);
+        if (!ok) break;
+        // only the columns that hold a query, in whole groups of 16
+        const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
+        const uint32_t idesc = idesc_f16kind_f32(E::kMmaFormat, BK, (cols + 15) & ~15, 0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == 1 && (tiles < 2 || blk < fb1)) continue;
+          const int buf = x * 2 + (sn[x] & 1);
+          if (sn[x] >= 2) {
+            ok = KVGQA_WAIT(&s_empty[buf], ((sn[x] >> 1) - 1) & 1);
+            if (!ok) break;
+          }
+          ++sn[x];
+          tc_fence_after();
+          const uint32_t k_addr = sbase + C::K_OFF + (ks * 2 + x) * C::TILE;
+          const uint32_t q_addr = sbase + C::Q_OFF + qs * C::TILE;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = (kk / 4) * SUB + (kk % 4) * 32;
+              umma_f16_ss(tmem + buf * BC, smem_desc_sw128(k_addr + o, 16, 1024), smem_desc_sw128(q_addr + o, 16, 1024),
+                          idesc, kk > 0);
+            }
+            umma_commit(&s_full[buf]);
+          }
+          __syncwarp();
+          issued = true;
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(&q_empty[qs]);
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(&k_empty[ks]);
+      __syncwarp();
+    }
+    if (*abort_flag && issued) {
+      if (elect_one()) umma_commit(drain);
+      __syncwarp();
+      volatile int none = 0;
+      mbar_wait_bounded(drain, 0, &none, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------ weights (warps 0-7)
+    const int x = warp >> 2;           // tile A or B
+    const int r = threadIdx.x & 127;   // cell of the tile == TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+    int n = 0, sn = 0;  // column blocks of the CTA, and those of this tile
+    bool ok = true;
+    for (; walk.ok && ok; walk.advance()) {
+      const int live = walk.live(x);
+      // Blocks that this tile does not use: their log sums are passed on.
+      const int fb = live > 0 ? walk.first_block(x) : walk.nblk;
+      for (int blk = walk.first_block(0); blk < fb && ok; ++blk, ++n) {
+        ok = __all_sync(FULLMASK, mbar_wait_bounded(&l_full[n % NL], (n / NL) & 1, abort_flag, p.status));
+        if (lane == 0) mbar_arrive(&l_empty[n % NL]);
+      }
+      if (!ok) break;
+      if (live <= 0) continue;  // the item has no tile B
+      const int cell = walk.kb * ITEM + x * BK + r;
+      float* dst = p.mass + (static_cast<size_t>(walk.a) * p.H_kv + walk.g) * p.mass_cells + cell;
+      const float before = r < live ? *dst : 0.f;
+      // column i of block blk sees this cell iff blk * BC + i >= c_min
+      const int c_min = max(cell - walk.off, 0) << p.gp_shift;
+      const int c_tile = max(walk.kb * ITEM + x * BK + live - 1 - walk.off, 0) << p.gp_shift;  // the tile's largest
+      float2 sum = make_float2(0.f, 0.f);
+      for (int blk = fb; blk < walk.nblk; ++blk, ++n, ++sn) {
+        const int buf = x * 2 + (sn & 1);
+        ok = __all_sync(FULLMASK, mbar_wait_bounded(&s_full[buf], (sn >> 1) & 1, abort_flag, p.status));
+        if (ok) ok = __all_sync(FULLMASK, mbar_wait_bounded(&l_full[n % NL], (n / NL) & 1, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        const float* ls = lse_s + (n % NL) * BC;
+        const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
+        const bool band = blk * BC < c_tile;
+        const int lo = c_min - blk * BC;
+#pragma unroll 1
+        for (int q = 0; q < cols; q += 32) {
+          uint32_t u[32];
+          tmem_ld32(tmem + lane_base + buf * BC + q, u);
+          tmem_wait_ld();
+          float* sv = reinterpret_cast<float*>(u);
+          if (band || q + 32 > cols) {  // columns that do not see the cell, or hold no query
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              sum.x += q + i >= lo && q + i < cols ? ex2(fmaf(sv[i], p.scale_log2, -ls[q + i])) : 0.f;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(ls + q + i);
+              const float2 xa = ffma2(make_float2(sv[i], sv[i + 1]), c2, make_float2(-l4.x, -l4.y));
+              const float2 xb = ffma2(make_float2(sv[i + 2], sv[i + 3]), c2, make_float2(-l4.z, -l4.w));
+              sum = fadd2(sum, make_float2(ex2(xa.x), ex2(xa.y)));
+              sum = fadd2(sum, make_float2(ex2(xb.x), ex2(xb.y)));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_empty[buf]);
+          mbar_arrive(&l_empty[n % NL]);
+        }
+      }
+      if (!ok) break;
+      if (r < live) *dst = before + (sum.x + sum.y);
+    }
+  }
+#undef KVGQA_WAIT
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == W_MMA) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+template <int D, bool F16>
+cudaError_t launch_d(const PagedMassParams& p, const CUtensorMap& mq, const CUtensorMap& mk, cudaStream_t stream) {
+  static std::once_flag flags[64];
+  static cudaError_t errs[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::call_once(flags[dev], [&] {
+    errs[dev] = cudaFuncSetAttribute(paged_mass_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     MCfg<D>::SMEM);
+  });
+  if (errs[dev] != cudaSuccess) return errs[dev];
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.num_ctas);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = MCfg<D>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_mass_kernel<D, F16>, p, mq, mk);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_mass(const PagedMassParams& params, cudaStream_t stream) {
+  if (params.m.A == 0 || params.m.N == 0) return cudaSuccess;
+  PagedMassParams p = params;
+  p.gp_shift = 0;
+  while ((1 << p.gp_shift) < p.G) ++p.gp_shift;
+  const int gp = 1 << p.gp_shift;
+  // A block's box holds no more tokens than any sequence has (in a power of
+  // two, and whole 8-row groups of the swizzle): a single token's block is its
+  // own heads, not 128 rows of its neighbours.
+  p.box_tokens = 1;
+  while (p.box_tokens * gp < BC && (p.box_tokens < p.m.max_query_len || p.box_tokens * gp < 8)) p.box_tokens *= 2;
+  auto enc = tma_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const CUtensorMapDataType type = p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t D = p.D, G = p.G, Hkv = p.H_kv, page = 1ull << p.m.page_shift;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  CUtensorMap mq, mk;
+  {
+    const cuuint64_t dims[4] = {D, G, Hkv, static_cast<cuuint64_t>(p.m.N)};
+    const cuuint64_t strides[3] = {D * 2, D * 2 * G, D * 2 * G * Hkv};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(gp), 1, static_cast<cuuint32_t>(p.box_tokens)};
+    if (enc(&mq, type, 4, const_cast<uint16_t*>(p.q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  {
+    const cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(p.m.P) * Hkv};
+    const cuuint64_t strides[2] = {D * 2, D * 2 * page};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page < BK ? page : BK), 1};
+    if (enc(&mk, type, 3, const_cast<uint16_t*>(p.k_cache), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (p.D == 128) return p.f16 ? launch_d<128, true>(p, mq, mk, stream) : launch_d<128, false>(p, mq, mk, stream);
+  if (p.D == 64) return p.f16 ? launch_d<64, true>(p, mq, mk, stream) : launch_d<64, false>(p, mq, mk, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvgqa

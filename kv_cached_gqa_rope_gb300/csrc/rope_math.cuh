@@ -8,6 +8,8 @@
 
 #include <cstdint>
 
+#include "elem.cuh"
+
 namespace kvgqa {
 
 struct __align__(16) CosSin {
@@ -135,6 +137,33 @@ __device__ __forceinline__ float rot_second(float x1, float x2, const CosSin& cs
   const float qe = __fmaf_rn(x1, cs.sh, -q);
   const float lo = __fmaf_rn(x2, cs.cl, __fmaf_rn(x1, cs.sl, __fadd_rn(pe, qe)));
   return __fadd_rn(__fadd_rn(p, q), lo);
+}
+
+// The cos/sin table is read eight consecutive entries at a time by lanes that
+// differ in which group of eight they read; one 16-byte pad after every eight
+// entries puts those lanes on different shared-memory banks.
+__device__ __forceinline__ int cs_slot(int i) { return i + (i >> 3); }
+
+// Rotate the 8 pairs (a[i], b[i]) held in two 16-byte chunks of the storage
+// type; each result is rounded once (nearest even) back to it.
+template <bool F16>
+__device__ __forceinline__ void rotate8(const uint4& a, const uint4& b, const CosSin* cs,
+                                        uint4& ya, uint4& yb) {
+  using E = Elem<F16>;
+  // cs points at the padded slot of pair 8c; the eight pairs follow contiguously
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+  const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+  uint32_t oa[4], ob[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float2 x1 = E::pair_to_f2(aw[w]);
+    const float2 x2 = E::pair_to_f2(bw[w]);
+    const CosSin c0 = cs[2 * w], c1 = cs[2 * w + 1];
+    oa[w] = E::pack2(rot_first(x1.x, x2.x, c0), rot_first(x1.y, x2.y, c1));
+    ob[w] = E::pack2(rot_second(x1.x, x2.x, c0), rot_second(x1.y, x2.y, c1));
+  }
+  ya = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+  yb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
 }
 
 }  // namespace kvgqa
