@@ -33,6 +33,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kCachedCells = 9216;  // 36 KB of keys beside the histogram: no more than a CTA may have by default
 
 // Keys in the order of the masses: NaN lowest, then -inf .. +inf, both zeros alike.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -49,7 +50,9 @@ __device__ __forceinline__ bool pages_ok(const PagedMeta& m, int a, int n) {
   return __syncthreads_and(ok);
 }
 
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
+  extern __shared__ uint32_t keys[];  // CACHED: the keys of all cells
   __shared__ int hist[kBins];
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ uint32_t sel_digit;
@@ -83,6 +86,16 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
     return;
   }
 
+  if constexpr (CACHED) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += kSelThreads) keys[i] = order_key(mass[i]);
+    __syncthreads();
+  }
+  auto key_of = [&](int i) {
+    if constexpr (CACHED) return keys[i];
+    else return order_key(mass[i]);
+  };
+
   // The smallest key that is kept among the old cells, and how many cells of
   // that very key are.
   const int old = n - p.recent;
@@ -97,8 +110,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
       shift -= bits;
       for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = tid; i < old; i += kSelThreads) {
-        const uint32_t k = order_key(mass[i]);
+        const uint32_t k = key_of(i);
         if ((k & above) == thr) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
       }
       __syncthreads();
@@ -133,12 +147,10 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
   const int S = ((n + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int s0 = warp * S, s1 = min(n, s0 + S);
   const bool any_old = p.keep > p.recent;
-  auto classify = [&](int i, bool& gt, bool& eq, float& x) {
+  auto classify = [&](int i, bool& gt, bool& eq) {
     gt = eq = false;
-    x = 0.f;
     if (i < s1) {
-      x = mass[i];
-      const uint32_t k = order_key(x);
+      const uint32_t k = key_of(i);
       gt = i >= old || (any_old && k > thr);
       eq = i < old && any_old && k == thr;
     }
@@ -146,8 +158,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
   int gts = 0, eqs = 0;
   for (int i = s0 + lane; i < s0 + S; i += 32) {
     bool gt, eq;
-    float x;
-    classify(i, gt, eq, x);
+    classify(i, gt, eq);
     gts += __popc(__ballot_sync(FULL, gt));
     eqs += __popc(__ballot_sync(FULL, eq));
   }
@@ -164,8 +175,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
   at += min(eq_before, need);
   for (int i = s0 + lane; i < s0 + S; i += 32) {
     bool gt, eq;
-    float x;
-    classify(i, gt, eq, x);
+    classify(i, gt, eq);
     const uint32_t below = (1u << lane) - 1;
     const uint32_t eqm = __ballot_sync(FULL, eq);
     const bool take = gt || (eq && eq_before + __popc(eqm & below) < need);
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
     if (take) {
       const int to = at + __popc(tm & below);
       kept[to] = i;
-      mass_out[to] = x;
+      mass_out[to] = mass[i];
     }
     at += __popc(tm);
     eq_before += __popc(eqm);
@@ -181,51 +191,73 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 4;  // 16-byte chunks per thread and batch
+constexpr int kMoveBatch = 4;    // 16-byte chunks per thread and batch
+constexpr int kTablePages = 2048;  // pages of the table kept in shared memory (more are looked up in L2)
 
-__global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const __grid_constant__ PagedEvictParams p,
-                                                                        int slices) {
+__global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const __grid_constant__ PagedEvictParams p,
+                                                                           int slices) {
+  __shared__ int pages[kTablePages];
   int b = blockIdx.x;
   const int slice = b % slices;
   b /= slices;
   uint16_t* cache = b & 1 ? p.v_cache : p.k_cache;
   b >>= 1;
   const int a = b / p.H_kv, g = b % p.H_kv;
+  const int shift = p.m.page_shift, page = 1 << shift;
+  const int n = p.m.kv_lengths[a];  // (an input of the call, like the table: not written by kernel 1)
+  bool ok = n > p.keep && n <= p.m.max_cells;
+  if (!ok) return;  // uniform
+  const int n_pages = (n + page - 1) >> shift;
+  for (int i = threadIdx.x; i < n_pages; i += kMoveThreads) {
+    const int pid = paged_page(p.m, a, i << shift);
+    ok = ok && pid >= 0;
+    if (i < kTablePages) pages[i] = pid;
+  }
+  if (!__syncthreads_and(ok)) return;
   pdl_wait();
-  const int n = p.m.kv_lengths[a];
-  if (n <= p.keep || n > p.m.max_cells || !pages_ok(p.m, a, n)) return;
   const int32_t* kept = p.kept + (static_cast<size_t>(a) * p.H_kv + g) * p.keep;
-  const int page = 1 << p.m.page_shift;
-  const int chunks = p.D / 8 / slices;  // 16-byte chunks of a row's slice (a power of two)
-  const int rows = kMoveThreads / chunks * kMoveBatch;  // rows of a batch
+  const int chunks = p.D / 8 / slices;              // 16-byte chunks of a row's slice (a power of two)
+  const int step = kMoveThreads / chunks;           // rows that the CTA covers at a time
+  const int rows = step * kMoveBatch;               // rows of a batch
   const int chunk = threadIdx.x % chunks, row = threadIdx.x / chunks;
+  uint16_t* base = cache + (slice * chunks + chunk) * 8;
   auto at = [&](int cell) {
-    return cache + ((static_cast<size_t>(paged_page(p.m, a, cell)) * p.H_kv + g) * page + (cell & (page - 1))) * p.D +
-           (slice * chunks + chunk) * 8;
+    const int i = cell >> shift;
+    const int pid = i < kTablePages ? pages[i] : paged_page(p.m, a, cell);
+    return base + ((static_cast<size_t>(pid) * p.H_kv + g) * page + (cell & (page - 1))) * p.D;
   };
-  uint4 x[2][kMoveBatch];
-  uint16_t* to[2][kMoveBatch];
-  auto load = [&](int base, uint4 (&v)[kMoveBatch], uint16_t* (&dst)[kMoveBatch]) {
+  // Batch k moves the kept cells k * rows + row, + step, ...; -1: none, or one
+  // that is in its place already.
+  auto sources = [&](int k, int (&from)[kMoveBatch]) {
 #pragma unroll
     for (int u = 0; u < kMoveBatch; ++u) {
-      const int i = base + row + u * (kMoveThreads / chunks);
-      dst[u] = nullptr;
-      if (i >= p.keep) continue;
-      const int from = kept[i];
-      if (from == i) continue;  // already in its place
-      dst[u] = at(i);
-      v[u] = *reinterpret_cast<const uint4*>(at(from));
+      const int i = k * rows + row + u * step;
+      from[u] = i < p.keep ? kept[i] : -1;
+      if (from[u] == i) from[u] = -1;
     }
   };
-  load(0, x[0], to[0]);
-  for (int base = 0; base < p.keep; base += 2 * rows) {
+  auto load = [&](const int (&from)[kMoveBatch], uint4 (&v)[kMoveBatch]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      load(base + (h + 1) * rows, x[h ^ 1], to[h ^ 1]);
-      __syncthreads();  // every read of this batch's cells is done
+    for (int u = 0; u < kMoveBatch; ++u)
+      if (from[u] >= 0) v[u] = *reinterpret_cast<const uint4*>(at(from[u]));
+  };
+  int from[kMoveBatch], next[kMoveBatch];
+  uint4 x[kMoveBatch], y[kMoveBatch];
+  sources(0, from);
+  load(from, x);
+  sources(1, next);
+  const int batches = (p.keep + rows - 1) / rows;
+  for (int k = 0; k < batches; ++k) {
+    load(next, y);  // batch k + 1
+    int after[kMoveBatch];
+    sources(k + 2, after);
+    __syncthreads();  // every read of batch k's cells, and those batch k overwrites, is done
 #pragma unroll
-      for (int u = 0; u < kMoveBatch; ++u)
-        if (to[h][u]) *reinterpret_cast<uint4*>(to[h][u]) = x[h][u];
+    for (int u = 0; u < kMoveBatch; ++u) {
+      if (from[u] >= 0) *reinterpret_cast<uint4*>(at(k * rows + row + u * step)) = x[u];
+      x[u] = y[u];
+      from[u] = next[u];
+      next[u] = after[u];
     }
   }
 }
@@ -235,10 +267,12 @@ __global__ void __launch_bounds__(kMoveThreads) paged_evict_move_kernel(const __
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   const long long heads = static_cast<long long>(p.m.A) * p.H_kv;
   if (heads == 0) return cudaSuccess;
-  // Slices of at least one 32-byte sector, until there are about four CTAs to
-  // an SM.
+  // Column slices until there are CTAs for several rounds of every SM, so that
+  // sequences of different lengths even out: down to 64 bytes, and to one
+  // 32-byte sector where the heads are too few to fill the GPU once.
   int slices = 1;
-  while (slices < p.D / 16 && heads * 2 * slices < 608) slices *= 2;
+  while (slices < p.D / 32 && heads * 2 * slices < 2400) slices *= 2;
+  if (heads * 2 * slices < 600) slices *= 2;
   if (heads * 2 * slices > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -249,8 +283,13 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_evict_select_kernel, p);
+  // The keys are kept in shared memory up to kCachedCells cells a row; longer rows are read from L2 in each pass.
+  const bool cached = p.mass_cells <= kCachedCells;
+  cfg.dynamicSmemBytes = cached ? static_cast<size_t>(p.mass_cells) * sizeof(uint32_t) : 0;
+  const cudaError_t e = cached ? cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<true>, p)
+                               : cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<false>, p);
   if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(static_cast<unsigned>(heads * 2 * slices));
   cfg.blockDim = dim3(kMoveThreads);
   return cudaLaunchKernelEx(&cfg, paged_evict_move_kernel, p, slices);

@@ -9,14 +9,18 @@
 // turned by are independent of each other.
 //
 // The kernel is bound by memory: every head of a token is read once and
-// written once (512 bytes per head at D = 128), and the angles are D/2 per
-// token whatever the heads.  One warp owns a token (or, with few tokens, a
-// share of its heads, so that the loads of a decode step spread over the GPU
-// and each warp waits for one round trip): it evaluates the D/2 angles two per
-// lane, then lane l keeps the cos/sin of its 8 pairs in registers and streams
-// heads l / (D/16), + 32 / (D/16), ..., 32 bytes in and out per head, with the
-// first heads' loads issued before the metadata and the angles are known.
-// V heads take the same path without the rotation.
+// written once (512 bytes per head at D = 128).  One warp takes kBatch rounds
+// of heads of one token (16 heads at D = 128), a single round trip: all its
+// loads are issued before the metadata and the angles are known.  It evaluates
+// the D/2 angles two per lane; lane l then holds the cos/sin of its 8 pairs in
+// registers and turns heads l / (D/16), + 32 / (D/16), ..., 32 bytes of each.
+// V heads take the same path without the rotation.  A token's angles are
+// evaluated once per warp that shares it, which costs less than the registers
+// and the waiting of one warp that walks all heads: the prefill of 16 x 1024
+// tokens with 32 + 8 + 8 heads took 94 us that way, with the angles as
+// double-float numbers, and @@ us (@@ TB/s) like this.  The angle is reduced
+// exactly (integers) and the rest is FP32: a turned value is off by at most
+// 2^-22 of its pair before it is rounded to the storage type.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,13 +52,34 @@ __device__ __forceinline__ int find_sequence(const PagedMeta& m, int n) {
   return lo;
 }
 
+// x1 cos - x2 sin and x2 cos + x1 sin of two neighbouring pairs.
+struct Turn2 {
+  float2 c, s, ns;  // cos, sin, -sin
+};
+template <bool F16>
+__device__ __forceinline__ void turn8(const uint4& a, const uint4& b, const Turn2 (&t)[4], uint4& ya, uint4& yb) {
+  using E = Elem<F16>;
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+  uint32_t oa[4], ob[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float2 x1 = E::pair_to_f2(aw[w]), x2 = E::pair_to_f2(bw[w]);
+    const float2 y1 = ffma2(x1, t[w].c, fmul2(x2, t[w].ns));
+    const float2 y2 = ffma2(x2, t[w].c, fmul2(x1, t[w].s));
+    oa[w] = E::pack2(y1.x, y1.y);
+    ob[w] = E::pack2(y2.x, y2.y);
+  }
+  ya = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+  yb = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kWarps * 32)
-paged_rope_kv_store_kernel(const __grid_constant__ PagedStoreParams p, int split, int heads_per, int trigger) {
+paged_rope_kv_store_kernel(const __grid_constant__ PagedStoreParams p, int split, int trigger) {
   constexpr int HALF = D / 2;
   constexpr int CH = D / 16;   // lanes that share a head: 8 pairs each
   constexpr int HL = 32 / CH;  // heads a warp covers at a time
-  __shared__ CosSin cs_s[kWarps][HALF + HALF / 8];
+  __shared__ float2 cs_s[kWarps][HALF];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   if (trigger) pdl_trigger();
@@ -62,28 +87,19 @@ paged_rope_kv_store_kernel(const __grid_constant__ PagedStoreParams p, int split
   const int n = static_cast<int>(item / split), part = static_cast<int>(item % split);
   if (n >= p.m.N) return;
   const int heads = p.H_q + 2 * p.H_kv, rot_heads = p.H_q + p.H_kv;
-  const int h_end = min(heads, (part + 1) * heads_per);
-  const int c = lane % CH, hl = lane / CH;
-  int h0 = part * heads_per + hl;
+  const int c = lane % CH, h0 = part * kBatch * HL + lane / CH;
 
-  auto src = [&](int h) -> const uint16_t* {
-    if (h < p.H_q) return p.q + n * p.q_stride + h * D;
-    if (h < rot_heads) return p.k + n * p.k_stride + (h - p.H_q) * D;
-    return p.v + n * p.v_stride + (h - rot_heads) * D;
-  };
   uint4 xa[kBatch], xb[kBatch];
-  auto load = [&]() {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h0 + b * HL;
-      if (h < h_end) {
-        const uint16_t* s = src(h) + c * 8;
-        xa[b] = *reinterpret_cast<const uint4*>(s);
-        xb[b] = *reinterpret_cast<const uint4*>(s + HALF);
-      }
-    }
-  };
-  load();
+  for (int b = 0; b < kBatch; ++b) {
+    const int h = h0 + b * HL;
+    if (h >= heads) continue;
+    const uint16_t* s = h < p.H_q ? p.q + n * p.q_stride + h * D
+                      : h < rot_heads ? p.k + n * p.k_stride + (h - p.H_q) * D
+                                      : p.v + n * p.v_stride + (h - rot_heads) * D;
+    xa[b] = *reinterpret_cast<const uint4*>(s + c * 8);
+    xb[b] = *reinterpret_cast<const uint4*>(s + HALF + c * 8);
+  }
 
   // The positions of this lane's pairs, and the token's cell.
   int pos[HALF / 32];
@@ -108,33 +124,29 @@ paged_rope_kv_store_kernel(const __grid_constant__ PagedStoreParams p, int split
   const size_t cell_off = (static_cast<size_t>(pid) * p.H_kv * page + (cell & (page - 1))) * D;
   const size_t head_step = static_cast<size_t>(page) * D;
 
-  CosSin* cs = cs_s[warp];
 #pragma unroll
   for (int u = 0; u < HALF / 32; ++u) {
     const int i = lane + 32 * u;
-    cs[cs_slot(i)] = rope_cos_sin(pos[u], p.freqs.frac[i], p.freqs.quad[i]);
+    cs_s[warp][i] = rope_cos_sin_f32(pos[u], p.freqs.frac[i], p.freqs.quad[i]);
   }
   __syncwarp();
-  CosSin mine_cs[8];
+  Turn2 t[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mine_cs[i] = cs[cs_slot(c * 8) + i];
-
-  for (;;) {
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(&cs_s[warp][c * 8 + 2 * i]);
+    t[i] = Turn2{make_float2(v.x, v.z), make_float2(v.y, v.w), make_float2(-v.y, -v.w)};
+  }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h0 + b * HL;
-      if (h >= h_end) continue;
-      uint16_t* dst = h < p.H_q ? p.q_out + (static_cast<size_t>(n) * p.H_q + h) * D
-                    : h < rot_heads ? p.k_cache + cell_off + (h - p.H_q) * head_step
-                                    : p.v_cache + cell_off + (h - rot_heads) * head_step;
-      uint4 ya = xa[b], yb = xb[b];
-      if (h < rot_heads) rotate8<F16>(xa[b], xb[b], mine_cs, ya, yb);
-      *reinterpret_cast<uint4*>(dst + c * 8) = ya;
-      *reinterpret_cast<uint4*>(dst + HALF + c * 8) = yb;
-    }
-    h0 += kBatch * HL;
-    if (h0 - hl >= h_end) break;
-    load();
+  for (int b = 0; b < kBatch; ++b) {
+    const int h = h0 + b * HL;
+    if (h >= heads) continue;
+    uint16_t* dst = h < p.H_q ? p.q_out + (static_cast<size_t>(n) * p.H_q + h) * D
+                  : h < rot_heads ? p.k_cache + cell_off + (h - p.H_q) * head_step
+                                  : p.v_cache + cell_off + (h - rot_heads) * head_step;
+    uint4 ya = xa[b], yb = xb[b];
+    if (h < rot_heads) turn8<F16>(xa[b], xb[b], t, ya, yb);
+    *reinterpret_cast<uint4*>(dst + c * 8) = ya;
+    *reinterpret_cast<uint4*>(dst + HALF + c * 8) = yb;
   }
 }
 
@@ -142,11 +154,7 @@ template <int D, bool F16>
 cudaError_t launch(const PagedStoreParams& p, cudaStream_t stream) {
   constexpr int HL = 32 / (D / 16);
   const int heads = p.H_q + 2 * p.H_kv;
-  // With fewer tokens than keep the GPU busy (two thousand warps), a token's
-  // heads are shared out in whole rounds.
-  const int rounds = (heads + HL * kBatch - 1) / (HL * kBatch);
-  const int split = std::max(1, std::min(rounds, 2048 / std::max(1, p.m.N)));
-  const int heads_per = (rounds + split - 1) / split * HL * kBatch;
+  const int split = (heads + HL * kBatch - 1) / (HL * kBatch);  // warps that share a token
   const long long items = static_cast<long long>(p.m.N) * split;
   const long long grid = (items + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -161,7 +169,7 @@ cudaError_t launch(const PagedStoreParams& p, cudaStream_t stream) {
   cfg.numAttrs = 1;
   // The next kernel may set itself up early only behind a short store: behind
   // a long one its CTAs would take SMs that this one's later CTAs need.
-  return cudaLaunchKernelEx(&cfg, paged_rope_kv_store_kernel<D, F16>, p, split, heads_per, grid <= 512 ? 1 : 0);
+  return cudaLaunchKernelEx(&cfg, paged_rope_kv_store_kernel<D, F16>, p, split, grid <= 512 ? 1 : 0);
 }
 
 }  // namespace

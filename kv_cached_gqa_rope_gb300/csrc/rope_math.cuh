@@ -116,6 +116,32 @@ __device__ __forceinline__ CosSin rope_cos_sin(int pos, uint64_t frac, uint32_t 
   return v;
 }
 
+// cos and sin of the same angle in FP32 (x = cos, y = sin), each within 2^-23:
+// the same exact reduction modulo a quarter turn, then the Taylor series up to
+// x^9 and x^10 (|x| <= pi/4: the terms left out are below 2e-9).
+__device__ __forceinline__ float2 rope_cos_sin_f32(int pos, uint64_t frac, uint32_t quad) {
+  const uint32_t n = static_cast<uint32_t>(pos);
+  const uint64_t lo = static_cast<uint64_t>(n) * static_cast<uint32_t>(frac);
+  const uint64_t hi = static_cast<uint64_t>(n) * static_cast<uint32_t>(frac >> 32);
+  const uint64_t f64 = lo + (hi << 32);
+  const uint32_t whole = static_cast<uint32_t>(hi >> 32) + (f64 < lo ? 1u : 0u) + n * quad;
+  const uint32_t q = (whole + static_cast<uint32_t>(f64 >> 63)) & 3u;
+  const float x = static_cast<float>(static_cast<int64_t>(f64)) *
+                  static_cast<float>(1.5707963267948966 / 18446744073709551616.0);  // pi/2 * 2^-64
+  const float y = x * x;
+  float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(s, y, 1.0f / 120.0f);
+  s = fmaf(s, y, -1.0f / 6.0f);
+  s = fmaf(s * y, x, x);
+  float c = fmaf(y, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  c = fmaf(c, y, -1.0f / 720.0f);
+  c = fmaf(c, y, 1.0f / 24.0f);
+  c = fmaf(c, y, -0.5f);
+  c = fmaf(c, y, 1.0f);
+  const float a = q & 1 ? s : c, b = q & 1 ? c : s;
+  return make_float2(q == 1 || q == 2 ? -a : a, q & 2 ? -b : b);
+}
+
 // x1 * C - x2 * S with C, S given as hi+lo pairs.  Products are split exactly
 // with FMA; intrinsics keep the compiler from contracting them differently,
 // so the BF16 result is one rounding of an almost exact value even where the
