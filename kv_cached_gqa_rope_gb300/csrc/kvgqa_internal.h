@@ -167,7 +167,7 @@ struct PagedAttentionParams {
   PagedMeta m;
   int H_q, H_kv, G, D, f16, num_ctas;
   int out_32b;                  // out is 32-byte aligned (set by the launcher)
-  int gp_shift;                 // log2 of the group size padded to a power of two (set by the launcher)
+  int gp_shift, box_tokens;     // log2 of the group size padded to a power of two, tokens of a query box (set by the launcher)
   float scale_log2;             // scale * log2(e)
 };
 // Workspace of the paged attention behind the status block.

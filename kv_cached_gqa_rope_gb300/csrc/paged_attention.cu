@@ -24,15 +24,19 @@
 //   warp 9      the same for the V tile; in a sequence's last tile it zeroes the
 //               rows behind the last cell, which may hold anything (a zero
 //               weight times a NaN is a NaN);
-//   warp 10     one thread issues tcgen05.mma: S_x = Q_x K^T into TMEM and
-//               O_x += P_x V with P_x read from TMEM (x = A, B);
+//   warps 10, 11 issue tcgen05.mma for A and for B: S_x = Q_x K^T into TMEM
+//               and O_x += P_x V with P_x read from TMEM;
 //   warps 0-3   softmax of tile A, warps 4-7 of tile B, one thread per row: FP32
 //               online softmax (the base follows the row maximum only when it
 //               grew by more than 2^8; O / l stays exact), P in the storage type
 //               written back over the S columns.  P's rounding is that of the
 //               tensor cores' operand type; the sum l is of the unrounded FP32
 //               weights.
-// While one tile's softmax works on its scores, the other tile's MMAs run.
+// While one tile's softmax works on its scores, the other tile's MMAs run.  A
+// block of at most 128 rows (a decode step, a short chunk, a prompt's last
+// tokens) has no tile B: there the two groups take the key tiles in turn, each
+// with its own running maximum, sum and accumulator, which group A joins at the
+// end; warps without a row of the sequence skip the softmax.
 // Long chunks are bound by the softmax's exponentials beside the MMAs, single
 // tokens by the stream of K and V.
 #include <cuda.h>
@@ -56,7 +60,7 @@ constexpr int BN = 128;        // keys of a tile
 constexpr int ROWS = 2 * BM;   // rows of a segment's block: tiles A and B
 constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
 constexpr int THREADS = 12 * 32;
-constexpr int W_K = 8, W_V = 9, W_MMA = 10;
+constexpr int W_K = 8, W_V = 9, W_MMA = 10;  // and W_MMA + 1
 // Register split (setmaxnreg): the launch gives every thread kLaunchRegs; the
 // role warpgroup drops to kRoleRegs so that the two softmax warpgroups can
 // hold a whole score row each.
@@ -77,6 +81,10 @@ struct PagedCut {
 // CTA b holds a segment that starts there, slot 2b one that started before.
 __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<size_t>(ROWS) * (D + 2); }
 
+// A value that every lane of the warp has, as one the compiler may keep in
+// uniform registers (the operands of tcgen05.mma live there).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(FULLMASK, v, 0); }
+
 template <int D>
 struct ACfg {
   static constexpr int NSUB = D / 64;
@@ -90,11 +98,12 @@ struct ACfg {
   static constexpr int STG_OFF = V_OFF + NV * TILE; // (and the schedule's scratch, before any output)
   static constexpr int BAR_OFF = STG_OFF + 8 * STG;
   // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
-  // s_full[2], p_full[2], o_done[2], v_land, drain (index [2] = tile A / B)
-  static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 8;
+  // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, drain[2] (index [2] = tile A / B)
+  static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 11;
   static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
-  static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // + alignment slack
+  static constexpr int ML_OFF = FLAG_OFF + 16;       // group B's m and l of a shared block, [2][BM] floats
+  static constexpr int SMEM = ML_OFF + 2 * BM * 4 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -191,6 +200,8 @@ struct PagedWalk {
   int first, ql, off;     // the sequence's first packed row, new tokens, cells before them
   int vlo, tiles, kend;   // the segment's virtual start, key tiles, last cell + 1
   int j, j_first, j_end;  // key tile, and this CTA's part of the segment
+  int par, slot;          // a block without tile B: the group its key tile goes to, its query buffer
+  bool two;               // whether the block has rows in tile B
   bool ok;
 
   __device__ __forceinline__ void load_seq() {
@@ -204,6 +215,7 @@ struct PagedWalk {
   __device__ __forceinline__ bool enter() {
     kend = off + min(ql, (b + 1) * block_tokens(*p));
     tiles = (kend + BN - 1) / BN;
+    two = (ql - b * block_tokens(*p)) << p->gp_shift > BM;
     const int lo = max(v0, vlo), hi = min(v1, vlo + tiles);
     j = j_first = lo - vlo;
     j_end = hi - vlo;
@@ -244,17 +256,30 @@ struct PagedWalk {
     }
     b = lo;
     vlo = v0 - rem + sum_units(*p, off, b);
+    par = slot = 0;
     ok = enter() || next_segment();
   }
   __device__ __forceinline__ bool fresh() const { return j == j_first; }
-  __device__ __forceinline__ bool last() const { return j == j_end - 1; }
-  // Whether the block has rows in tile B.
-  __device__ __forceinline__ bool dual() const { return (ql - b * block_tokens(*p)) << p->gp_shift > BM; }
+  // Whether the block has rows in tile B.  If not, the two groups take turns
+  // with its key tiles.
+  __device__ __forceinline__ bool dual() const { return two; }
+  __device__ __forceinline__ int parts() const { return j_end - j_first; }  // key tiles of this part
   __device__ __forceinline__ bool whole() const { return vlo >= v0 && vlo + tiles <= v1; }
   __device__ __forceinline__ int tok0() const { return b * block_tokens(*p); }
+  // The next key tile.
   __device__ __forceinline__ void advance() {
-    if (j < j_end - 1) ++j;
-    else ok = next_segment();
+    if (j < j_end - 1) {
+      ++j;
+      if (!dual()) par ^= 1;
+    } else {
+      if (!dual()) par ^= 1, slot ^= 1;
+      ok = next_segment();
+    }
+  }
+  // The next segment, from the first key tile of this one (softmax groups, MMA issuers).
+  __device__ __forceinline__ void advance_segment() {
+    if (!dual()) par ^= parts() & 1, slot ^= 1;
+    ok = next_segment();
   }
 };
 
@@ -300,10 +325,12 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   uint64_t* p_full = s_full + 2;       // [tile]
   uint64_t* o_done = p_full + 2;       // [tile]
   uint64_t* v_land = o_done + 2;       // a sequence's last V tile has landed
-  uint64_t* drain = v_land + 1;
+  uint64_t* ml_full = v_land + 1;      // group B's m and l of a shared block are written
+  uint64_t* ml_done = ml_full + 1;     // group A has read them and group B's accumulator
+  uint64_t* drain = ml_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;  // (roles, hence addresses, the same in a warp)
   PagedCut* cut = static_cast<PagedCut*>(p.cuts) + blockIdx.x;
 
   pdl_wait();
@@ -317,21 +344,24 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);
     }
     for (int s = 0; s < C::NV; ++s) {
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 1);
+      mbar_init(&q_empty[x], 2);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);  // one arrival per softmax warp
       mbar_init(&o_done[x], 1);
     }
     mbar_init(v_land, 1);
-    mbar_init(drain, 1);
+    mbar_init(ml_full, 4);  // one arrival per warp of the group
+    mbar_init(ml_done, 4);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -342,8 +372,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t sbase = smem_u32(smem);
+  const uint32_t tmem = uniform(*tmem_slot);
+  const uint32_t sbase = uniform(smem_u32(smem));
 
   if (warp >= 8) {
   regs_dec<kRoleRegs>();
@@ -353,21 +383,23 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     // ------------------------------------------------------------ Q and K producer
     const uint64_t pol_q = l2_evict_first_policy();
     const uint64_t pol_kv = l2_evict_last_policy();  // re-read by the sequence's other blocks
-    int it = 0, qn[2] = {0, 0};  // K tiles, and Q tiles (A, B) loaded so far
-    auto load_q = [&](int x) -> bool {
-      if (qn[x] >= 1 && !KVGQA_WAIT(&q_empty[x], (qn[x] - 1) & 1)) return false;
+    int it = 0, qn[2] = {0, 0};  // K tiles, and query tiles in each buffer, loaded so far
+    // Query tile x of the block (0: A, 1: B) into buffer i.
+    auto load_q = [&](int i, int x) -> bool {
+      int& n = i == 0 ? qn[0] : qn[1];
+      if (n >= 1 && !KVGQA_WAIT(&q_empty[i], (n - 1) & 1)) return false;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[x], BM * D * 2);
+        mbar_arrive_expect_tx(&q_full[i], (p.box_tokens << p.gp_shift) * D * 2);
         for (int sub = 0; sub < C::NSUB; ++sub)
-          tma_load_4d(smem + C::Q_OFF + x * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g,
-                      walk.first + walk.tok0() + x * (BM >> p.gp_shift), &q_full[x], pol_q);
+          tma_load_4d(smem + C::Q_OFF + i * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g,
+                      walk.first + walk.tok0() + x * (BM >> p.gp_shift), &q_full[i], pol_q);
       }
-      ++qn[x];
+      ++n;
       return true;
     };
     for (; walk.ok; walk.advance()) {
-      const bool fresh = walk.fresh();
-      if (fresh && !load_q(0)) break;
+      const bool fresh = walk.fresh(), dual = walk.dual();
+      if (fresh && !load_q(dual ? 0 : walk.slot, 0)) break;
       const int s = it % C::NK;
       const TileBoxes t = tile_boxes(walk, lane);
       if (it >= C::NK && !KVGQA_WAIT(&k_empty[s], ((it / C::NK) - 1) & 1)) break;
@@ -379,7 +411,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           tma_load_3d(st + sub * SUB, &map_k, sub * 64, t.c1, t.c2, &k_full[s], pol_kv);
       }
       ++it;
-      if (fresh && walk.dual() && !load_q(1)) break;
+      if (fresh && dual && !load_q(1, 1)) break;
     }
     __syncwarp();
     if (*abort_flag) {  // let the copies in flight land
@@ -426,79 +458,96 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       for (int t = it - C::NV < 0 ? 0 : it - C::NV; t < it; ++t)
         mbar_wait_bounded(&v_full[t % C::NV], (t / C::NV) & 1, &none, nullptr);
     }
-  } else if (warp == W_MMA) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop; one elected lane issues each group of
-    // MMAs and its commits.  Step t: P.V of tile t, then S of tile t + 1, for
-    // A, then for B (where the tile's segment has rows in B).
+  } else {
+    // ------------------------------------------------------------ MMA issuers
+    // Warp W_MMA + x issues the MMAs of group x: P.V of its last key tile, then
+    // S of its next (in that order, since P lies over S).  Each issuer's waits
+    // and bookkeeping pass while the tensor cores work on what the other has
+    // issued: their queue is short, and one issuer for both groups left it empty
+    // for a third of the time.  The whole warp runs the loop; one elected lane
+    // issues the MMAs and their commits.  A stage is released by two arrivals:
+    // one of each issuer, or two of the only one that uses it.
     constexpr uint32_t IDESC_QK = idesc_f16kind_f32(E::kMmaFormat, BM, BN, 0);
     constexpr uint32_t IDESC_PV = idesc_f16kind_f32(E::kMmaFormat, BM, D, 1);
+    const uint32_t x = warp - W_MMA;
+    const uint32_t s_tm = tmem + x * BN, o_tm = tmem + (2 + x) * BN;
     bool issued = false, ok = true;
-    int qn = 0, qnb = 0;         // Q tiles A and B consumed
-    int pn = 0, pnb = 0;         // P tiles A and B consumed
-    bool first = false, dual = false;  // of tile t
-    for (int t = -1; ok; ++t) {
-      const bool more = walk.ok;
-      const int sv = t % C::NV, kn = (t + 1) % C::NK;
-      if (t >= 0) ok = KVGQA_WAIT(&v_full[sv], (t / C::NV) & 1);
-      if (ok && more) ok = KVGQA_WAIT(&k_full[kn], ((t + 1) / C::NK) & 1);
-      if (!ok) break;
-      const uint32_t v_addr = sbase + C::V_OFF + sv * C::TILE;
-      const uint32_t k_addr = sbase + C::K_OFF + kn * C::TILE;
-      const bool n_first = more && walk.fresh(), n_last = more && walk.last(), n_dual = more && walk.dual();
+    int tiles = 0;            // key tiles of the segments before this one
+    int n = 0;                // tiles of this group whose S has been issued
+    int qn[2] = {0, 0};       // query tiles in each buffer so far
+    int prev = -1;            // the tile whose P.V is next
+    bool prev_first = false, prev_alone = false;
+    auto pv = [&]() -> bool {  // O_x (+)= P_x V of tile `prev`
+      const int sv = prev % C::NV;
+      if (!KVGQA_WAIT(&v_full[sv], (prev / C::NV) & 1)) return false;
+      if (!KVGQA_WAIT(&p_full[x], (n - 1) & 1)) return false;
+      tc_fence_after();
+      const uint32_t v_lo = smem_desc_lo(sbase + C::V_OFF + sv * C::TILE, SUB);
+      if (elect_one()) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (t >= 0 && (x == 0 || dual)) {
-          int& n = x == 0 ? pn : pnb;
-          ok = KVGQA_WAIT(&p_full[x], n & 1);
-          if (!ok) break;
-          ++n;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < BN / 16; ++ks)
-              umma_f16_ts(tmem + (2 + x) * BN, tmem + x * BN + ks * 8, smem_desc_sw128(v_addr + ks * 2048, SUB, 1024),
-                          IDESC_PV, (ks > 0 || !first) ? 1u : 0u);
-            umma_commit(&o_done[x]);
-            if (x == 1 || !dual) umma_commit(&v_empty[sv]);
-          }
-          __syncwarp();
-        }
-        if (more && (x == 0 || n_dual)) {
-          if (n_first) {
-            int& n = x == 0 ? qn : qnb;
-            ok = KVGQA_WAIT(&q_full[x], n & 1);
-            if (!ok) break;
-            ++n;
-          }
-          tc_fence_after();
-          const uint32_t q_addr = sbase + C::Q_OFF + x * C::TILE;
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t o = (ks / 4) * SUB + (ks % 4) * 32;
-              umma_f16_ss(tmem + x * BN, smem_desc_sw128(q_addr + o, 16, 1024), smem_desc_sw128(k_addr + o, 16, 1024),
-                          IDESC_QK, ks > 0);
-            }
-            umma_commit(&s_full[x]);
-            if (n_last) umma_commit(&q_empty[x]);
-            if (x == 1 || !n_dual) umma_commit(&k_empty[kn]);
-          }
-          __syncwarp();
-          issued = true;
-        }
+        for (int ks = 0; ks < BN / 16; ++ks)
+          umma_f16_ts_lo(o_tm, s_tm + ks * 8, v_lo + ks * 128, IDESC_PV, (ks > 0 || !prev_first) ? 1u : 0u);
+        umma_commit(&o_done[x]);
+        umma_commit(&v_empty[sv]);
+        if (prev_alone) umma_commit(&v_empty[sv]);
       }
-      if (!more) break;
-      first = n_first;
-      dual = n_dual;
-      walk.advance();
+      __syncwarp();
+      return true;
+    };
+    for (; walk.ok && ok; walk.advance_segment()) {
+      const bool dual = walk.dual();
+      const int parts = walk.parts(), step = dual ? 1 : 2, from = dual || walk.par == static_cast<int>(x) ? 0 : 1;
+      const uint32_t i = dual ? x : uniform(walk.slot);  // the query buffer
+      int& qi = i == 0 ? qn[0] : qn[1];
+      for (int k = from; k < parts; k += step) {
+        if (prev >= 0) {
+          ok = pv();
+          if (!ok) break;
+        }
+        const int t = tiles + k, kn = t % C::NK;
+        if (k == from) ok = KVGQA_WAIT(&q_full[i], qi & 1);
+        ok = ok && KVGQA_WAIT(&k_full[kn], (t / C::NK) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t k_lo = smem_desc_lo(sbase + C::K_OFF + kn * C::TILE, 16);
+        const uint32_t q_lo = smem_desc_lo(sbase + C::Q_OFF + i * C::TILE, 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t o = (ks / 4) * (SUB >> 4) + (ks % 4) * (32 >> 4);
+            umma_f16_ss_lo(s_tm, q_lo + o, k_lo + o, IDESC_QK, ks > 0);
+          }
+          umma_commit(&s_full[x]);
+          umma_commit(&k_empty[kn]);
+          if (!dual) umma_commit(&k_empty[kn]);
+          if (k + step >= parts) {
+            umma_commit(&q_empty[i]);
+            if (dual || parts == 1) umma_commit(&q_empty[i]);
+          }
+        }
+        __syncwarp();
+        issued = true;
+        prev = t;
+        prev_first = k == from;
+        prev_alone = !dual;
+        ++n;
+      }
+      // (the buffer's count goes on for every segment that uses it, whether or not this issuer has a tile of it)
+      if (dual) {
+        ++qn[0];
+        ++qn[1];
+      } else {
+        ++qi;
+      }
+      tiles += parts;
     }
+    if (ok && prev >= 0) pv();
     if (*abort_flag && issued) {
       // let every MMA issued so far finish before TMEM is released
-      if (elect_one()) umma_commit(drain);
+      if (elect_one()) umma_commit(&drain[x]);
       __syncwarp();
       volatile int none = 0;
-      mbar_wait_bounded(drain, 0, &none, nullptr);
+      mbar_wait_bounded(&drain[x], 0, &none, nullptr);
     }
   }
 #undef KVGQA_WAIT
@@ -507,7 +556,6 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     regs_inc<kSoftmaxRegs>();
     const int x = warp >> 2;           // tile A or B
     const int r = threadIdx.x & 127;   // row of the tile == TMEM lane
-    const int row_tok = (x * BM + r) >> p.gp_shift;  // token of the row, within the block
     const int row_g = r & ((1 << p.gp_shift) - 1);   // head of the group
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + x * BN;
@@ -515,14 +563,28 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     const float c = p.scale_log2;
     const float ce = c > 0.f ? c : 1.f;
     float m_ref = -INFINITY, l = 0.f;
-    int t = 0;  // tiles of this group so far
-    for (; walk.ok; walk.advance()) {
-      if (x == 1 && !walk.dual()) continue;  // no rows in tile B
-      const bool first = walk.fresh(), last = walk.last();
-      // Row r sees column i of the tile iff i <= thr.
-      const int thr0 = walk.off + walk.tok0() - walk.j * BN;
+    float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
+    int t = 0, t_other = 0;  // tiles of this group and of the other so far
+    int n_shared = 0;        // shared parts so far
+    for (; walk.ok; walk.advance_segment()) {
+      const bool dual = walk.dual();
+      // In a block without tile B both groups hold its 128 rows and take its
+      // key tiles in turn.
+      const int row0 = dual ? x * BM : 0;
+      const int row_tok = (row0 + r) >> p.gp_shift;   // token of the row, within the block
+      const int warp_tok = (row0 + (warp & 3) * 32) >> p.gp_shift;  // and of the warp's first row
+      const bool live = walk.tok0() + warp_tok < walk.ql;  // the warp has rows of the sequence
+      const int step = dual ? 1 : 2;
+      const int seen = walk.off + walk.tok0();        // row r sees the cells up to seen + row_tok
+      bool first = true;
+      int j = walk.j_first + (dual || walk.par == x ? 0 : 1);
+      bool ok = true;
+      for (; j < walk.j_end; j += step) {
+      const int thr0 = seen - j * BN;  // column i of the tile is seen iff i <= thr
       const int thr = thr0 + row_tok;
-      if (!__all_sync(FULLMASK, mbar_wait_bounded(&s_full[x], t & 1, abort_flag, p.status))) break;
+      ok = __all_sync(FULLMASK, mbar_wait_bounded(&s_full[x], t & 1, abort_flag, p.status));
+      if (!ok) break;
+      if (live) {
       tc_fence_after();
       // Scores enter the softmax as s * ce with ce > 0 (a scale that is not
       // positive is folded into the scores first).
@@ -535,7 +597,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
 #pragma unroll
         for (int i = 0; i < BN; ++i) sv[i] *= c;
       }
-      if (thr0 + ((x * BM) >> p.gp_shift) < BN - 1) {  // a tile that reaches past a row's cell
+      if (thr0 + warp_tok < BN - 1) {  // a tile that reaches past a row's cell
 #pragma unroll
         for (int i = 0; i < BN; ++i) sv[i] = i <= thr ? sv[i] : -INFINITY;
       }
@@ -590,39 +652,87 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       }
       tmem_wait_st();
       l += ls.x + ls.y;
+      }
       // Each warp arrives once: every lane's TMEM stores are complete and
       // fenced before the warp synchronises, then lane 0 arrives.
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[x]);
-
-      if (last) {
-        // ---------------------------------------------------- end of this part of the segment
-        if (!__all_sync(FULLMASK, mbar_wait_bounded(&o_done[x], t & 1, abort_flag, p.status))) break;
-        tc_fence_after();
-        const int tok = walk.tok0() + row_tok;
-        const bool row_ok = tok < walk.ql && row_g < p.G;
+      ++t;
+      first = false;
+      }
+      if (!ok) break;
+      // ------------------------------------------------------ end of this part of the segment
+      // A block without tile B whose part has two tiles or more is finished by
+      // group A, which reads both accumulators (the lanes of tensor memory are
+      // the same) once group B has left its m and l.
+      const bool shared = !dual && walk.parts() > 1;
+      t_other += dual ? walk.parts() : (walk.parts() + (walk.par != x)) / 2;
+      if (first) continue;  // no tile of this part was this group's
+      float wa = 1.f, wb = 0.f;  // weights of the two accumulators
+      if (shared) {
+        const int ph = n_shared++ & 1;
+        if (x == 1) {
+          ml[r] = m_ref;
+          ml[BM + r] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_full);
+          if (!__all_sync(FULLMASK, mbar_wait_bounded(ml_done, ph, abort_flag, p.status))) break;
+          continue;
+        }
+        if (!__all_sync(FULLMASK, mbar_wait_bounded(ml_full, ph, abort_flag, p.status)) ||
+            !__all_sync(FULLMASK, mbar_wait_bounded(&o_done[1], (t_other - 1) & 1, abort_flag, p.status)))
+          break;
+        const float mb = ml[r], lb = ml[BM + r];
+        const float m = fmaxf(m_ref, mb);
+        // (a group that saw none of the row's cells has m = -inf and weighs nothing)
+        wa = m_ref == -INFINITY ? 0.f : ex2(m_ref - m);
+        wb = mb == -INFINITY ? 0.f : ex2(mb - m);
+        l = l * wa + lb * wb;
+        m_ref = m;
+      }
+      const bool done = __all_sync(FULLMASK, mbar_wait_bounded(&o_done[x], (t - 1) & 1, abort_flag, p.status));
+      tc_fence_after();
+      const int tok = walk.tok0() + row_tok;
+      const bool row_ok = tok < walk.ql && row_g < p.G;
+      const uint32_t ob_col = tmem + lane_base + 3 * BN;
+      // 32 values of the row from column q on: the merged accumulators
+      auto read_o = [&](int q, uint32_t (&v)[32]) {
+        tmem_ld32(o_col + q, v);
+        tmem_wait_ld();
+        if (shared) {
+          uint32_t w[32];
+          tmem_ld32(ob_col + q, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float o = wa > 0.f ? __uint_as_float(v[i]) * wa : 0.f;
+            v[i] = __float_as_uint(wb > 0.f ? fmaf(__uint_as_float(w[i]), wb, o) : o);
+          }
+        }
+      };
+      if (done && live) {
         if (walk.whole()) {
           const float inv = 1.f / l;
           const size_t head = static_cast<size_t>(walk.first + tok) * p.H_q + walk.g * p.G + row_g;
           // This warp's 32 rows go out through shared memory and a TMA store
           // when all of its tokens belong to the sequence; else the rows that
           // do take direct stores.
-          const int warp_tok = (x * BM + (warp & 3) * 32) >> p.gp_shift;
           const bool via_tma = walk.tok0() + warp_tok + (32 >> p.gp_shift) <= walk.ql;
           unsigned char* stg = smem + C::STG_OFF + warp * C::STG;
           uint16_t* dst = p.out + head * D;
           if (row_ok && p.lse) p.lse[head] = (m_ref + log2f(l)) * 0.6931471805599453f;
 #pragma unroll
           for (int sub = 0; sub < C::NSUB; ++sub) {  // 64 output values of the row at a time
-            uint32_t v[64];
-            tmem_ld32(o_col + sub * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
-            tmem_ld32(o_col + sub * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-            tmem_wait_ld();
             uint32_t w[32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              w[k] = E::pack2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[32];
+              read_o(sub * 64 + half * 32, v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[half * 16 + k] = E::pack2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+            }
             if (via_tma) {
               if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
               __syncwarp();
@@ -653,8 +763,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         } else {
           const bool starts = walk.vlo >= walk.v0;
           float* slot = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + starts) * slot_floats(D);
-          const int row = x * BM + r;
-          if (starts && threadIdx.x == 0) {
+          const int row = row0 + r;
+          if (starts && row == 0) {
             cut->tok = walk.first + walk.tok0();
             cut->g = walk.g;
             cut->last = (walk.vlo + walk.tiles - 1) / range.w;
@@ -667,8 +777,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
 #pragma unroll 1
           for (int q = 0; q < D / 32; ++q) {
             uint32_t v[32];
-            tmem_ld32(o_col + q * 32, v);
-            tmem_wait_ld();
+            read_o(q * 32, v);
             if (row_ok) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
@@ -678,7 +787,12 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           }
         }
       }
-      ++t;
+      if (!done) break;
+      if (shared) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ml_done);
+      }
     }
   }
 
@@ -752,7 +866,7 @@ cudaError_t make_maps(const PagedAttentionParams& p, Maps* m) {
   for (int t = 0; t < 2; ++t) {  // q, and out in boxes of 32 rows
     const cuuint64_t dims[4] = {D, G, Hkv, static_cast<cuuint64_t>(p.m.N)};
     const cuuint64_t strides[3] = {D * 2, D * 2 * G, D * 2 * G * Hkv};
-    const cuuint32_t box[4] = {64, gp, 1, (t == 0 ? BM : 32) / gp};
+    const cuuint32_t box[4] = {64, gp, 1, t == 0 ? static_cast<cuuint32_t>(p.box_tokens) : 32 / gp};
     if (enc(t == 0 ? &m->q : &m->o, type, 4, t == 0 ? const_cast<uint16_t*>(p.q) : p.out, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -829,6 +943,11 @@ cudaError_t launch_paged_attention(const PagedAttentionParams& params, cudaStrea
   p.out_32b = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
   p.gp_shift = 0;
   while ((1 << p.gp_shift) < p.G) ++p.gp_shift;
+  // A query tile's box holds no more tokens than any sequence has (as a power
+  // of two): a single token's tile is its own heads, and the rows behind them
+  // are whatever the buffer held, which no other row sees.
+  p.box_tokens = 1;
+  while (p.box_tokens << p.gp_shift < BM && p.box_tokens < p.m.max_query_len) p.box_tokens *= 2;
   Maps m;
   const cudaError_t e = make_maps(p, &m);
   if (e != cudaSuccess) return e;
