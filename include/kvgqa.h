@@ -435,9 +435,10 @@ kvgqa_status paged_rope_kv_store_out_(const kvgqa_tensor* q, const kvgqa_tensor*
 
 /* Workspace of paged_gqa_attention_out_ on `device`: the status block and the
  * partial results of sequences that are split over the GPU (it depends on the
- * device's SM count, not on the number or length of the sequences).  Nothing in
- * it but the status word has to be zero before a call.  Calls that may overlap
- * on the GPU need workspaces of their own. */
+ * device's SM count, not on the number or length of the sequences).  It must be
+ * zero-filled before the first call; every call that completes leaves it ready
+ * for the next (after KVGQA_FLAG_TIMEOUT, kvgqa_read_status() zero-fills it).
+ * Calls that may overlap on the GPU need workspaces of their own. */
 kvgqa_status paged_gqa_attention_workspace_size(int64_t H_q, int64_t H_kv, int64_t D, int32_t device, size_t* bytes);
 
 /*

@@ -67,7 +67,8 @@ constexpr int W_K = 8, W_V = 9, W_MMA = 10;  // and W_MMA + 1
 constexpr int kLaunchRegs = 168, kRoleRegs = 72, kSoftmaxRegs = 216;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kRoleRegs <= THREADS * kLaunchRegs, "register split");
 constexpr int TMEM_COLS = 512; // S_A, S_B, O_A, O_B: 128 columns each
-constexpr int UNITS_MIN = 3;   // fewest units a CTA is given
+constexpr int UNITS_MIN = 4;   // fewest units a CTA is given
+constexpr int kSmallRows = 32; // rows of a block in the SMALL form (one warp's)
 constexpr unsigned FULLMASK = 0xffffffffu;
 
 // A segment cut at a CTA boundary, noted by the CTA where it starts.
@@ -76,6 +77,8 @@ struct PagedCut {
   int tok;     // first packed token
   int g;       // KV head
   int last;    // last CTA that holds a part of it
+  int done;    // SMALL: parts finished so far (zero between calls)
+  int pad[3];
 };
 // One partial result: O[ROWS][D], then m[ROWS], then l[ROWS]; slot 2b + 1 of
 // CTA b holds a segment that starts there, slot 2b one that started before.
@@ -85,49 +88,71 @@ __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<siz
 // uniform registers (the operands of tcgen05.mma live there).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(FULLMASK, v, 0); }
 
-template <int D>
+// SMALL: no block of the call has more than kSmallRows rows (decode steps, a
+// few tokens per sequence), so the stream of K and V is all there is to it.  The
+// query buffers hold those rows alone, the output needs no staging, and the
+// shared memory that leaves deepens the K and V rings.  (The tensor cores read
+// 128 rows from a query buffer's start on; those behind it are whatever lies
+// there, and no row sees another.)
+template <int D, bool SMALL>
 struct ACfg {
   static constexpr int NSUB = D / 64;
-  static constexpr int TILE = NSUB * SUB;           // one Q, K or V tile
-  static constexpr int NK = D == 128 ? 2 : 4;       // K stages
-  static constexpr int NV = D == 128 ? 2 : 4;       // V stages
-  static constexpr int Q_OFF = 0;                   // Q_A, Q_B
-  static constexpr int K_OFF = 2 * TILE;
+  static constexpr int TILE = NSUB * SUB;           // one K or V tile
+  static constexpr int QSUB = SMALL ? kSmallRows * 128 : SUB;
+  static constexpr int QTILE = NSUB * QSUB;         // one query tile
+  static constexpr int NK = 2 * 128 / D;            // K stages
+  static constexpr int NV = (SMALL ? 4 : 2) * 128 / D;  // V stages (a V tile is held longer: through the softmax)
+  static_assert(NK % 2 == 0 && NV % 2 == 0, "a stage's tiles alternate with the groups (see the walk)");
+  static constexpr int Q_OFF = 0;                   // two query buffers
+  static constexpr int K_OFF = 2 * QTILE;
   static constexpr int V_OFF = K_OFF + NK * TILE;
-  static constexpr int STG = 32 * 128;              // output staging of one softmax warp
-  static constexpr int STG_OFF = V_OFF + NV * TILE; // (and the schedule's scratch, before any output)
-  static constexpr int BAR_OFF = STG_OFF + 8 * STG;
+  static constexpr int STG = SMALL ? 0 : 32 * 128;  // output staging of one softmax warp
+  static constexpr int STG_OFF = V_OFF + NV * TILE;
+  static constexpr int ML_OFF = STG_OFF + 8 * STG;  // group B's m and l of a shared block (and the schedule's scratch)
+  static constexpr int BAR_OFF = ML_OFF + 2 * BM * 4;
   // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
   // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, drain[2] (index [2] = tile A / B)
   static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 11;
   static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
-  static constexpr int ML_OFF = FLAG_OFF + 16;       // group B's m and l of a shared block, [2][BM] floats
-  static constexpr int SMEM = ML_OFF + 2 * BM * 4 + 1024;  // + alignment slack
+  static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { return ROWS >> p.gp_shift; }
-// Virtual units of a segment that ends with the block's (i - 1)-th successor
-// of token off (i = b + 1): at least its key tiles and one.
-__device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int i) {
-  return off / BN + 2 + (i * block_tokens(p) + BN - 1) / BN;
+// Virtual units: kPair per key tile of a block with both query tiles, one per
+// key tile of a block with one (measured: 1.9 us and about 1 us), kEnd for a
+// segment's start and end.  A segment is given at least the units of its key
+// tiles, in a form whose sums over a sequence's blocks are closed: off / BN + 1 +
+// ceil((b + 1) tokens / BN) tiles for block b of a sequence with off cells
+// before its new tokens.  All blocks of a sequence but the last have two query tiles.
+constexpr int kPair = 2, kEnd = 1;
+__device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int b, int weight) {
+  return weight * (off / BN + 1 + ((b + 1) * block_tokens(p) + BN - 1) / BN) + kEnd;
 }
-// The sum of seg_units(off, i) over i = 1 .. n, in closed form.
-__device__ __forceinline__ int sum_units(const PagedAttentionParams& p, int off, int n) {
-  int s;
+// The units of a sequence's first n blocks, all of them pairs.
+__device__ __forceinline__ int pair_units(const PagedAttentionParams& p, int off, int n) {
+  int s;  // the sum of ceil(i tokens / BN) over i = 1 .. n
   if (p.gp_shift == 0) {
     s = n * (n + 1);                           // 256 tokens a block: 2i
   } else {
     const int sh = p.gp_shift - 1, m = n >> sh, r = n & ((1 << sh) - 1);
     s = ((m * (m + 1)) >> 1 << sh) + r * (m + 1);  // 2^sh blocks to a key tile: ceil(i / 2^sh)
   }
-  return n * (off / BN + 2) + s;
+  return kPair * (n * (off / BN + 1) + s) + kEnd * n;
+}
+__device__ __forceinline__ int block_weight(const PagedAttentionParams& p, int ql, int b) {
+  return (ql - b * block_tokens(p)) << p.gp_shift > BM ? kPair : 1;
+}
+// The units of one KV head of a sequence.
+__device__ __forceinline__ int head_units(const PagedAttentionParams& p, int ql, int off) {
+  if (ql == 0) return 0;
+  const int b = (ql - 1) / block_tokens(p);  // the last block
+  return pair_units(p, off, b) + seg_units(p, off, b, block_weight(p, ql, b));
 }
 __device__ __forceinline__ int seq_units(const PagedAttentionParams& p, const PagedSeq& s) {
-  const int tb = block_tokens(p);
-  return p.H_kv * sum_units(p, s.kl - s.ql, (s.ql + tb - 1) / tb);
+  return p.H_kv * head_units(p, s.ql, s.kl - s.ql);
 }
 
 // The range [v0, v1) of virtual units of this CTA and the sequence v0 falls
@@ -199,9 +224,9 @@ struct PagedWalk {
   int a, g, b, nblk;      // segment: sequence, KV head, block of the sequence's nblk
   int first, ql, off;     // the sequence's first packed row, new tokens, cells before them
   int vlo, tiles, kend;   // the segment's virtual start, key tiles, last cell + 1
+  int weight;             // units of a key tile
   int j, j_first, j_end;  // key tile, and this CTA's part of the segment
-  int par, slot;          // a block without tile B: the group its key tile goes to, its query buffer
-  bool two;               // whether the block has rows in tile B
+  int ring, slot;         // key tiles before this one; a block without tile B: its query buffer
   bool ok;
 
   __device__ __forceinline__ void load_seq() {
@@ -215,15 +240,16 @@ struct PagedWalk {
   __device__ __forceinline__ bool enter() {
     kend = off + min(ql, (b + 1) * block_tokens(*p));
     tiles = (kend + BN - 1) / BN;
-    two = (ql - b * block_tokens(*p)) << p->gp_shift > BM;
-    const int lo = max(v0, vlo), hi = min(v1, vlo + tiles);
-    j = j_first = lo - vlo;
-    j_end = hi - vlo;
-    return lo < hi;
+    weight = block_weight(*p, ql, b);
+    // the key tiles whose first unit lies in [v0, v1)
+    const int lo = max(v0 - vlo, 0), hi = v1 - vlo;
+    j = j_first = weight == 1 ? lo : (lo + kPair - 1) / kPair;
+    j_end = min(tiles, weight == 1 ? hi : (hi + kPair - 1) / kPair);
+    return j < j_end;
   }
   __device__ bool next_segment() {
     for (;;) {
-      vlo += seg_units(*p, off, b + 1);
+      vlo += seg_units(*p, off, b, weight);
       if (vlo >= v1) return false;
       if (++b == nblk) {
         b = 0;
@@ -245,40 +271,45 @@ struct PagedWalk {
     a = r.a;
     load_seq();
     int rem = v0 - r.pre;
-    const int head = sum_units(*p, off, nblk);
+    const int head = head_units(*p, ql, off);
     g = rem / head;
     rem -= g * head;
     int lo = 0, hi = nblk - 1;  // the block whose units hold v0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sum_units(*p, off, mid) <= rem) lo = mid;
+      if (pair_units(*p, off, mid) <= rem) lo = mid;
       else hi = mid - 1;
     }
     b = lo;
-    vlo = v0 - rem + sum_units(*p, off, b);
-    par = slot = 0;
+    vlo = v0 - rem + pair_units(*p, off, b);
+    ring = slot = 0;
     ok = enter() || next_segment();
   }
   __device__ __forceinline__ bool fresh() const { return j == j_first; }
   // Whether the block has rows in tile B.  If not, the two groups take turns
-  // with its key tiles.
-  __device__ __forceinline__ bool dual() const { return two; }
+  // with its key tiles: the group is the parity of the tile's place in the rings,
+  // so that with an even number of stages a stage's tiles of such blocks are all
+  // of one group.
+  __device__ __forceinline__ bool dual() const { return weight != 1; }
   __device__ __forceinline__ int parts() const { return j_end - j_first; }  // key tiles of this part
-  __device__ __forceinline__ bool whole() const { return vlo >= v0 && vlo + tiles <= v1; }
+  __device__ __forceinline__ bool whole() const { return parts() == tiles; }
+  __device__ __forceinline__ int last_unit() const { return vlo + weight * (tiles - 1); }
   __device__ __forceinline__ int tok0() const { return b * block_tokens(*p); }
+  __device__ __forceinline__ int group() const { return ring & 1; }
   // The next key tile.
   __device__ __forceinline__ void advance() {
+    ++ring;
     if (j < j_end - 1) {
       ++j;
-      if (!dual()) par ^= 1;
     } else {
-      if (!dual()) par ^= 1, slot ^= 1;
+      if (!dual()) slot ^= 1;
       ok = next_segment();
     }
   }
   // The next segment, from the first key tile of this one (softmax groups, MMA issuers).
   __device__ __forceinline__ void advance_segment() {
-    if (!dual()) par ^= parts() & 1, slot ^= 1;
+    ring += parts();
+    if (!dual()) slot ^= 1;
     ok = next_segment();
   }
 };
@@ -304,12 +335,67 @@ __device__ __forceinline__ TileBoxes tile_boxes(const PagedWalk& w, int lane) {
   return t;
 }
 
+// Atomic add with release and acquire semantics at GPU scope.
+__device__ __forceinline__ int atomic_add_acq_rel_gpu(int* ptr, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], %2;" : "=r"(old) : "l"(ptr), "r"(v) : "memory");
+  return old;
+}
+
+// One warp merges the parts b0 .. b1 of a block of `rows` <= 32 rows (read past
+// L1) and writes out and lse.  Up to 8 lanes share a row, each taking 16 of its
+// values at a time.
 template <int D, bool F16>
+__device__ __forceinline__ void merge_small(const PagedAttentionParams& p, int tok0, int rows, int g, int b0, int b1) {
+  using E = Elem<F16>;
+  const int lane = threadIdx.x & 31;
+  const int share = rows > 16 ? 1 : rows > 8 ? 2 : rows > 4 ? 4 : 8;
+  const int row = lane / share, col0 = lane % share * 16;
+  const int gi = row & ((1 << p.gp_shift) - 1);
+  if (row >= rows || gi >= p.G) return;
+  const float* slot0 = p.partials + (static_cast<size_t>(b0) * 2 + 1) * slot_floats(D);
+  auto part = [&](int b) { return b == b0 ? slot0 : p.partials + static_cast<size_t>(b) * 2 * slot_floats(D); };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int b = b0; b <= b1; ++b) M = fmaxf(M, __ldcg(part(b) + ROWS * D + row));
+  const size_t head = static_cast<size_t>(tok0 + (row >> p.gp_shift)) * p.H_q + g * p.G + gi;
+  for (int col = col0; col < D; col += share * 16) {
+    float l = 0.f, acc[16] = {};
+#pragma unroll 2
+    for (int b = b0; b <= b1; ++b) {
+      const float* s = part(b);
+      const float m = __ldcg(s + ROWS * D + row), lb = __ldcg(s + ROWS * D + ROWS + row);
+      float4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = __ldcg(reinterpret_cast<const float4*>(s + row * D + col) + k);
+      if (m == -INFINITY) continue;  // this part saw none of the row's cells
+      const float w = exp2f(m - M);
+      l += w * lb;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        acc[4 * k] += w * o[k].x;
+        acc[4 * k + 1] += w * o[k].y;
+        acc[4 * k + 2] += w * o[k].z;
+        acc[4 * k + 3] += w * o[k].w;
+      }
+    }
+    const float inv = 1.f / l;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = E::pack2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + col);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (col == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <int D, bool F16, bool SMALL>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const __grid_constant__ CUtensorMap map_o) {
-  using C = ACfg<D>;
+  using C = ACfg<D, SMALL>;
   using E = Elem<F16>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -336,7 +422,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   pdl_wait();
   if (threadIdx.x == 0) cut->rows = 0;
   Range range;
-  if (!find_range(p, reinterpret_cast<int*>(smem + C::STG_OFF), range)) return;  // uniform
+  if (!find_range(p, reinterpret_cast<int*>(smem + C::ML_OFF), range)) return;  // uniform
   PagedWalk walk;
   walk.init(&p, range);
   if (!walk.ok) return;  // uniform: nothing but padding in this range
@@ -391,14 +477,25 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       if (lane == 0) {
         mbar_arrive_expect_tx(&q_full[i], (p.box_tokens << p.gp_shift) * D * 2);
         for (int sub = 0; sub < C::NSUB; ++sub)
-          tma_load_4d(smem + C::Q_OFF + i * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g,
+          tma_load_4d(smem + C::Q_OFF + i * C::QTILE + sub * C::QSUB, &map_q, sub * 64, 0, walk.g,
                       walk.first + walk.tok0() + x * (BM >> p.gp_shift), &q_full[i], pol_q);
       }
       ++n;
       return true;
     };
+    bool turns = false;  // the last tile went to one group
     for (; walk.ok; walk.advance()) {
       const bool fresh = walk.fresh(), dual = walk.dual();
+      if (dual && turns) {
+        // Both groups wait for every tile of this block, but of the last tiles
+        // each knows its own only, and a barrier's parity does not tell a phase
+        // from the one two before it: let the rings run dry first.
+        bool dry = true;
+        for (int u = max(it - C::NK, 0); u < it && dry; ++u) dry = KVGQA_WAIT(&k_empty[u % C::NK], (u / C::NK) & 1);
+        for (int u = max(it - C::NV, 0); u < it && dry; ++u) dry = KVGQA_WAIT(&v_empty[u % C::NV], (u / C::NV) & 1);
+        if (!dry) break;
+      }
+      turns = !dual;
       if (fresh && !load_q(dual ? 0 : walk.slot, 0)) break;
       const int s = it % C::NK;
       const TileBoxes t = tile_boxes(walk, lane);
@@ -472,58 +569,83 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     const uint32_t x = warp - W_MMA;
     const uint32_t s_tm = tmem + x * BN, o_tm = tmem + (2 + x) * BN;
     bool issued = false, ok = true;
-    int tiles = 0;            // key tiles of the segments before this one
     int n = 0;                // tiles of this group whose S has been issued
     int qn[2] = {0, 0};       // query tiles in each buffer so far
     int prev = -1;            // the tile whose P.V is next
     bool prev_first = false, prev_alone = false;
-    auto pv = [&]() -> bool {  // O_x (+)= P_x V of tile `prev`
-      const int sv = prev % C::NV;
-      if (!KVGQA_WAIT(&v_full[sv], (prev / C::NV) & 1)) return false;
-      if (!KVGQA_WAIT(&p_full[x], (n - 1) & 1)) return false;
-      tc_fence_after();
-      const uint32_t v_lo = smem_desc_lo(sbase + C::V_OFF + sv * C::TILE, SUB);
-      if (elect_one()) {
+    // O_x (+)= P_x V of tile `prev`, by the elected lane
+    auto issue_pv = [&]() {
+      const uint32_t v_lo = smem_desc_lo(sbase + C::V_OFF + prev % C::NV * C::TILE, SUB);
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          umma_f16_ts_lo(o_tm, s_tm + ks * 8, v_lo + ks * 128, IDESC_PV, (ks > 0 || !prev_first) ? 1u : 0u);
+      for (int ks = 0; ks < BN / 16; ++ks)
+        umma_f16_ts_lo(o_tm, s_tm + ks * 8, v_lo + ks * 128, IDESC_PV, (ks > 0 || !prev_first) ? 1u : 0u);
+    };
+    auto release_v = [&]() {
+      uint64_t* free = &v_empty[prev % C::NV];
+      umma_commit(free);
+      if (prev_alone) umma_commit(free);
+    };
+    auto wait_p = [&]() -> bool {
+      return KVGQA_WAIT(&v_full[prev % C::NV], (prev / C::NV) & 1) && KVGQA_WAIT(&p_full[x], (n - 1) & 1);
+    };
+    auto finish_prev = [&]() -> bool {  // P.V of tile `prev`, if there is one
+      if (prev < 0) return true;
+      if (!wait_p()) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_pv();
         umma_commit(&o_done[x]);
-        umma_commit(&v_empty[sv]);
-        if (prev_alone) umma_commit(&v_empty[sv]);
+        release_v();
       }
       __syncwarp();
+      prev = -1;
       return true;
     };
     for (; walk.ok && ok; walk.advance_segment()) {
       const bool dual = walk.dual();
-      const int parts = walk.parts(), step = dual ? 1 : 2, from = dual || walk.par == static_cast<int>(x) ? 0 : 1;
+      const int parts = walk.parts(), step = dual ? 1 : 2, from = dual || walk.group() == static_cast<int>(x) ? 0 : 1;
       const uint32_t i = dual ? x : uniform(walk.slot);  // the query buffer
-      int& qi = i == 0 ? qn[0] : qn[1];
+      // A segment's last P.V waits for nothing of the next segment.
+      ok = finish_prev();
+      // Every issuer waits for every query tile and releases it, used or not,
+      // so that neither misses a phase.
+      for (uint32_t u = 0; u < 2 && ok; ++u) {
+        if (!dual && u != i) continue;
+        ok = KVGQA_WAIT(&q_full[u], (u == 0 ? qn[0] : qn[1]) & 1);
+        if (u == 0) ++qn[0];
+        else ++qn[1];
+        if (ok && lane == 0 && (u != i || from >= parts)) mbar_arrive(&q_empty[u]);
+      }
+      if (!ok) break;
       for (int k = from; k < parts; k += step) {
-        if (prev >= 0) {
-          ok = pv();
-          if (!ok) break;
-        }
-        const int t = tiles + k, kn = t % C::NK;
-        if (k == from) ok = KVGQA_WAIT(&q_full[i], qi & 1);
-        ok = ok && KVGQA_WAIT(&k_full[kn], (t / C::NK) & 1);
+        const int t = walk.ring + k, kn = t % C::NK;
+        // Both groups at work on each tile: its K has long landed, so it is
+        // waited for first and P.V and S go out without a gap.  The groups in
+        // turn: the stream of K and V is the bound, and P.V does not wait for
+        // a K tile that may still be on its way (its stage would be refilled
+        // later for it).
+        const bool together = dual && prev >= 0;
+        if (!together && !(ok = finish_prev())) break;
+        ok = KVGQA_WAIT(&k_full[kn], (t / C::NK) & 1) && (!together || wait_p());
         if (!ok) break;
         tc_fence_after();
         const uint32_t k_lo = smem_desc_lo(sbase + C::K_OFF + kn * C::TILE, 16);
-        const uint32_t q_lo = smem_desc_lo(sbase + C::Q_OFF + i * C::TILE, 16);
+        const uint32_t q_lo = smem_desc_lo(sbase + C::Q_OFF + i * C::QTILE, 16);
         if (elect_one()) {
+          if (together) {
+            issue_pv();
+            umma_commit(&o_done[x]);  // (before the scores': a group that has seen those finds o_done a phase on)
+          }
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t o = (ks / 4) * (SUB >> 4) + (ks % 4) * (32 >> 4);
-            umma_f16_ss_lo(s_tm, q_lo + o, k_lo + o, IDESC_QK, ks > 0);
+            const uint32_t o = (ks % 4) * (32 >> 4);
+            umma_f16_ss_lo(s_tm, q_lo + (ks / 4) * (C::QSUB >> 4) + o, k_lo + (ks / 4) * (SUB >> 4) + o, IDESC_QK, ks > 0);
           }
           umma_commit(&s_full[x]);
           umma_commit(&k_empty[kn]);
           if (!dual) umma_commit(&k_empty[kn]);
-          if (k + step >= parts) {
-            umma_commit(&q_empty[i]);
-            if (dual || parts == 1) umma_commit(&q_empty[i]);
-          }
+          if (together) release_v();
+          if (k + step >= parts) umma_commit(&q_empty[i]);
         }
         __syncwarp();
         issued = true;
@@ -532,16 +654,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         prev_alone = !dual;
         ++n;
       }
-      // (the buffer's count goes on for every segment that uses it, whether or not this issuer has a tile of it)
-      if (dual) {
-        ++qn[0];
-        ++qn[1];
-      } else {
-        ++qi;
-      }
-      tiles += parts;
     }
-    if (ok && prev >= 0) pv();
+    if (ok) finish_prev();
     if (*abort_flag && issued) {
       // let every MMA issued so far finish before TMEM is released
       if (elect_one()) umma_commit(&drain[x]);
@@ -577,7 +691,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       const int step = dual ? 1 : 2;
       const int seen = walk.off + walk.tok0();        // row r sees the cells up to seen + row_tok
       bool first = true;
-      int j = walk.j_first + (dual || walk.par == x ? 0 : 1);
+      int j = walk.j_first + (dual || walk.group() == x ? 0 : 1);
       bool ok = true;
       for (; j < walk.j_end; j += step) {
       const int thr0 = seen - j * BN;  // column i of the tile is seen iff i <= thr
@@ -667,7 +781,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       // group A, which reads both accumulators (the lanes of tensor memory are
       // the same) once group B has left its m and l.
       const bool shared = !dual && walk.parts() > 1;
-      t_other += dual ? walk.parts() : (walk.parts() + (walk.par != x)) / 2;
+      t_other += dual ? walk.parts() : (walk.parts() + (walk.group() != x)) / 2;
       if (first) continue;  // no tile of this part was this group's
       float wa = 1.f, wb = 0.f;  // weights of the two accumulators
       if (shared) {
@@ -718,7 +832,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           // This warp's 32 rows go out through shared memory and a TMA store
           // when all of its tokens belong to the sequence; else the rows that
           // do take direct stores.
-          const bool via_tma = walk.tok0() + warp_tok + (32 >> p.gp_shift) <= walk.ql;
+          const bool via_tma = !SMALL && walk.tok0() + warp_tok + (32 >> p.gp_shift) <= walk.ql;
           unsigned char* stg = smem + C::STG_OFF + warp * C::STG;
           uint16_t* dst = p.out + head * D;
           if (row_ok && p.lse) p.lse[head] = (m_ref + log2f(l)) * 0.6931471805599453f;
@@ -764,10 +878,10 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           const bool starts = walk.vlo >= walk.v0;
           float* slot = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + starts) * slot_floats(D);
           const int row = row0 + r;
-          if (starts && row == 0) {
+          if (!SMALL && starts && row == 0) {
             cut->tok = walk.first + walk.tok0();
             cut->g = walk.g;
-            cut->last = (walk.vlo + walk.tiles - 1) / range.w;
+            cut->last = walk.last_unit() / range.w;
             cut->rows = min(ROWS, (walk.ql - walk.tok0()) << p.gp_shift);
           }
           if (row_ok) {
@@ -783,6 +897,20 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
               for (int k = 0; k < 8; ++k)
                 *reinterpret_cast<uint4*>(slot + row * D + q * 32 + k * 4) =
                     make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+          }
+          if constexpr (SMALL) {
+            // One warp holds all rows of the block; whichever of its parts is
+            // written last merges them.
+            __threadfence();
+            __syncwarp();
+            const int b0 = walk.vlo / range.w, b1 = walk.last_unit() / range.w;
+            int* count = &static_cast<PagedCut*>(p.cuts)[b0].done;
+            int before = 0;
+            if (lane == 0) before = atomic_add_acq_rel_gpu(count, 1);
+            if (__shfl_sync(FULLMASK, before, 0) == b1 - b0) {
+              merge_small<D, F16>(p, walk.first, min(walk.ql << p.gp_shift, kSmallRows), walk.g, b0, b1);
+              if (lane == 0) *count = 0;  // ready for the next call
             }
           }
         }
@@ -808,7 +936,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
 // CTA (b, y): row group y of the cut segment that starts in CTA b of the
 // attention kernel, one warp per row.  A part whose maximum is -inf saw none
 // of the row's cells and weighs nothing.
-constexpr int kMergeWarps = 8, kMergeGroups = 8;
+constexpr int kMergeWarps = 8;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttentionParams p) {
@@ -817,7 +945,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   pdl_wait();
   const int b0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedCut cut = static_cast<const PagedCut*>(p.cuts)[b0];
-  for (int row = blockIdx.y * kMergeWarps + warp; row < cut.rows; row += kMergeGroups * kMergeWarps) {
+  for (int row = blockIdx.y * kMergeWarps + warp; row < cut.rows; row += gridDim.y * kMergeWarps) {
     const int gi = row & ((1 << p.gp_shift) - 1);
     if (gi >= p.G) continue;
     auto part = [&](int b) { return p.partials + (static_cast<size_t>(b) * 2 + (b == b0)) * slot_floats(D); };
@@ -885,8 +1013,9 @@ cudaError_t make_maps(const PagedAttentionParams& p, Maps* m) {
   return cudaSuccess;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool SMALL>
 cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t stream) {
+  using C = ACfg<D, SMALL>;
   static std::once_flag flags[64];
   static cudaError_t errs[64];
   int dev = 0;
@@ -894,11 +1023,11 @@ cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t 
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::call_once(flags[dev], [&] {
-    errs[dev] = cudaFuncSetAttribute(paged_attention_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     ACfg<D>::SMEM);
+    const auto kernel = paged_attention_kernel<D, F16, SMALL>;
+    errs[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     // setmaxnreg.inc is only satisfied if the launch hands out kLaunchRegs per thread.
     cudaFuncAttributes attr;
-    if (errs[dev] == cudaSuccess) errs[dev] = cudaFuncGetAttributes(&attr, paged_attention_kernel<D, F16>);
+    if (errs[dev] == cudaSuccess) errs[dev] = cudaFuncGetAttributes(&attr, kernel);
     if (errs[dev] == cudaSuccess && attr.numRegs < kLaunchRegs) errs[dev] = cudaErrorInvalidConfiguration;
   });
   if (errs[dev] != cudaSuccess) return errs[dev];
@@ -908,16 +1037,25 @@ cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.num_ctas);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = ACfg<D>::SMEM;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, F16>, p, m.q, m.k, m.v, m.o);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(p.num_ctas, kMergeGroups);
+  e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, F16, SMALL>, p, m.q, m.k, m.v, m.o);
+  if (e != cudaSuccess || SMALL) return e;
+  // One row to a warp, as far as the segments' blocks can have them.
+  const int64_t rows = std::min<int64_t>(ROWS, static_cast<int64_t>(p.m.max_query_len) << p.gp_shift);
+  cfg.gridDim = dim3(p.num_ctas, static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F16>, p);
+}
+
+template <int D>
+cudaError_t launch_width(const PagedAttentionParams& p, const Maps& m, cudaStream_t stream) {
+  if (static_cast<int64_t>(p.m.max_query_len) << p.gp_shift <= kSmallRows)
+    return p.f16 ? launch_d<D, true, true>(p, m, stream) : launch_d<D, false, true>(p, m, stream);
+  return p.f16 ? launch_d<D, true, false>(p, m, stream) : launch_d<D, false, false>(p, m, stream);
 }
 
 }  // namespace
@@ -951,8 +1089,8 @@ cudaError_t launch_paged_attention(const PagedAttentionParams& params, cudaStrea
   Maps m;
   const cudaError_t e = make_maps(p, &m);
   if (e != cudaSuccess) return e;
-  if (p.D == 128) return p.f16 ? launch_d<128, true>(p, m, stream) : launch_d<128, false>(p, m, stream);
-  if (p.D == 64) return p.f16 ? launch_d<64, true>(p, m, stream) : launch_d<64, false>(p, m, stream);
+  if (p.D == 128) return launch_width<128>(p, m, stream);
+  if (p.D == 64) return launch_width<64>(p, m, stream);
   return cudaErrorInvalidValue;
 }
 
