@@ -111,8 +111,8 @@ struct ACfg {
   static constexpr int ML_OFF = STG_OFF + 8 * STG;  // group B's m and l of a shared block (and the schedule's scratch)
   static constexpr int BAR_OFF = ML_OFF + 2 * BM * 4;
   // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
-  // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, drain[2] (index [2] = tile A / B)
-  static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 11;
+  // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, part_full[2], drain[2] (index [2] = tile A / B)
+  static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 13;
   static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
   static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // + alignment slack
@@ -164,55 +164,65 @@ struct Range {
 __device__ bool find_range(const PagedAttentionParams& p, int* scratch, Range& r) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = THREADS / 32;
-  int mine = 0, bad = 0;
-  for (int a = tid; a < p.m.A; a += THREADS) {
-    const PagedSeq s = paged_seq(p.m, a);
-    bad |= !s.ok;
-    mine += seq_units(p, s);
-  }
+  // Sums over chunks of one sequence per thread.  The last chunk's prefix stays
+  // in registers: with no more sequences than threads that is all there is.
+  int before_chunk = 0, units = 0, excl = 0, total = 0;
+  bool bad = false;
+  const int chunks = (p.m.A + THREADS - 1) / THREADS;
+  auto scan = [&](int chunk) {  // exclusive prefix of this thread's sequence, and the total up to the chunk's end
+    const int a = chunk * THREADS + tid;
+    PagedSeq s{};
+    if (a < p.m.A) {
+      s = paged_seq(p.m, a);
+      bad = bad || !s.ok;
+    }
+    units = a < p.m.A ? seq_units(p, s) : 0;
+    int incl = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(FULLMASK, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (chunk > 0) __syncthreads();  // the last chunk's sums have been read
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    before_chunk = total;
+    excl = before_chunk + incl - units;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int t = scratch[w];
+      if (w < warp) excl += t;
+      total += t;
+    }
+  };
+  for (int c = 0; c < chunks; ++c) scan(c);
   if (blockIdx.x == 0 && bad) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(FULLMASK, mine, o);
-  if (lane == 0) scratch[warp] = mine;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) total += scratch[w];
   r.w = max((total + p.num_ctas - 1) / p.num_ctas, UNITS_MIN);
   // (num_ctas ranges of w units hold the total; a product past 2^31 would mean v0 >= total)
   const long long v0 = static_cast<long long>(blockIdx.x) * r.w;
   if (v0 >= total) return false;
   r.v0 = static_cast<int>(v0);
   r.v1 = min(r.v0 + r.w, total);
-  int carry = 0;
-  for (int base = 0; base < p.m.A; base += THREADS) {
-    const int a = base + tid;
-    const int u = a < p.m.A ? seq_units(p, paged_seq(p.m, a)) : 0;
-    int incl = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(FULLMASK, incl, o);
-      if (lane >= o) incl += t;
+  int* found = scratch + NW;
+  if (chunks == 1) {
+    if (units > 0 && excl <= r.v0 && r.v0 < excl + units) {
+      found[0] = tid;
+      found[1] = excl;
     }
+  } else {
+    total = 0;
     __syncthreads();
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int before = carry;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const int t = scratch[w];
-      if (w < warp) before += t;
-      carry += t;
-    }
-    const int excl = before + incl - u;
-    if (u > 0 && excl <= r.v0 && r.v0 < excl + u) {
-      scratch[NW] = a;
-      scratch[NW + 1] = excl;
+    for (int c = 0; c < chunks; ++c) {
+      scan(c);
+      if (units > 0 && excl <= r.v0 && r.v0 < excl + units) {
+        found[0] = c * THREADS + tid;
+        found[1] = excl;
+      }
     }
   }
   __syncthreads();
-  r.a = scratch[NW];
-  r.pre = scratch[NW + 1];
+  r.a = found[0];
+  r.pre = found[1];
   return true;
 }
 
@@ -413,12 +423,18 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   uint64_t* v_land = o_done + 2;       // a sequence's last V tile has landed
   uint64_t* ml_full = v_land + 1;      // group B's m and l of a shared block are written
   uint64_t* ml_done = ml_full + 1;     // group A has read them and group B's accumulator
-  uint64_t* drain = ml_done + 1;
+  uint64_t* part_full = ml_done + 1;   // SMALL: the partial result in slot 0, 1 is written
+  uint64_t* drain = part_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;  // (roles, hence addresses, the same in a warp)
   PagedCut* cut = static_cast<PagedCut*>(p.cuts) + blockIdx.x;
 
+  if (warp == W_K && lane == 0) {
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+  }
   pdl_wait();
   if (threadIdx.x == 0) cut->rows = 0;
   Range range;
@@ -440,12 +456,14 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 2);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);  // one arrival per softmax warp
+      mbar_init(&p_full[x], SMALL ? 1 : 4);  // one arrival per softmax warp that works
       mbar_init(&o_done[x], 1);
     }
     mbar_init(v_land, 1);
-    mbar_init(ml_full, 4);  // one arrival per warp of the group
-    mbar_init(ml_done, 4);
+    mbar_init(ml_full, SMALL ? 1 : 4);
+    mbar_init(ml_done, SMALL ? 1 : 4);
+    mbar_init(&part_full[0], 1);
+    mbar_init(&part_full[1], 1);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
@@ -668,6 +686,29 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
     regs_inc<kSoftmaxRegs>();
+    if (SMALL && (warp & 3) != 0) {
+      // A small block's rows are one warp's (0 of its group).  Warp 1 counts the
+      // CTA's partial results and merges a segment whose parts are complete: its
+      // fence and its atomics would hold up the next segment elsewhere.
+      if (warp == 1) {
+        for (; walk.ok; walk.advance_segment()) {
+          if (walk.whole()) continue;
+          const bool starts = walk.vlo >= walk.v0;
+          if (!__all_sync(FULLMASK, mbar_wait_bounded(&part_full[starts], 0, abort_flag, p.status))) break;
+          __threadfence();
+          __syncwarp();
+          const int b0 = walk.vlo / range.w, b1 = walk.last_unit() / range.w;
+          int* count = &static_cast<PagedCut*>(p.cuts)[b0].done;
+          int before = 0;
+          if (lane == 0) before = atomic_add_acq_rel_gpu(count, 1);
+          if (__shfl_sync(FULLMASK, before, 0) == b1 - b0) {
+            merge_small<D, F16>(p, walk.first, min(walk.ql << p.gp_shift, kSmallRows), walk.g, b0, b1);
+            if (lane == 0) *count = 0;  // ready for the next call
+          }
+          __syncwarp();
+        }
+      }
+    } else {
     const int x = warp >> 2;           // tile A or B
     const int r = threadIdx.x & 127;   // row of the tile == TMEM lane
     const int row_g = r & ((1 << p.gp_shift) - 1);   // head of the group
@@ -825,6 +866,13 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           }
         }
       };
+      auto release_b = [&]() {  // group B's accumulator has been read
+        if (shared) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ml_done);
+        }
+      };
       if (done && live) {
         if (walk.whole()) {
           const float inv = 1.f / l;
@@ -847,6 +895,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
               for (int k = 0; k < 16; ++k)
                 w[half * 16 + k] = E::pack2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
             }
+            if (sub == C::NSUB - 1) release_b();
             if (via_tma) {
               if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
               __syncwarp();
@@ -899,28 +948,16 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
                     make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
           }
+          release_b();
           if constexpr (SMALL) {
-            // One warp holds all rows of the block; whichever of its parts is
-            // written last merges them.
-            __threadfence();
             __syncwarp();
-            const int b0 = walk.vlo / range.w, b1 = walk.last_unit() / range.w;
-            int* count = &static_cast<PagedCut*>(p.cuts)[b0].done;
-            int before = 0;
-            if (lane == 0) before = atomic_add_acq_rel_gpu(count, 1);
-            if (__shfl_sync(FULLMASK, before, 0) == b1 - b0) {
-              merge_small<D, F16>(p, walk.first, min(walk.ql << p.gp_shift, kSmallRows), walk.g, b0, b1);
-              if (lane == 0) *count = 0;  // ready for the next call
-            }
+            if (lane == 0) mbar_arrive(&part_full[starts]);
           }
         }
       }
       if (!done) break;
-      if (shared) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ml_done);
-      }
+      if (!live) release_b();
+    }
     }
   }
 
