@@ -821,7 +821,7 @@ PagedViews paged_meta(kvgqa::PagedMeta* m, const kvgqa_tensor* query_starts, boo
 // over all of a sequence's cells.
 void check_paged_work(const kvgqa::PagedMeta& m, int64_t H_kv, int64_t block) {
   const int64_t blocks = m.N / block + m.A, units = m.max_cells / 128 + m.max_query_len / 128 + 8;
-  if (!product_below({blocks, units, H_kv}, 1ll << 29))
+  if (!product_below({blocks, units, H_kv, 2}, 1ll << 30))
     fail(KVGQA_EUNSUPPORTED, "too much work for one call (tokens, cells and heads); split the batch");
 }
 

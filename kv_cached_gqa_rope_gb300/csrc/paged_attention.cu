@@ -68,6 +68,7 @@ constexpr int kLaunchRegs = 168, kRoleRegs = 72, kSoftmaxRegs = 216;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kRoleRegs <= THREADS * kLaunchRegs, "register split");
 constexpr int TMEM_COLS = 512; // S_A, S_B, O_A, O_B: 128 columns each
 constexpr int UNITS_MIN = 4;   // fewest units a CTA is given
+constexpr int kSeqs = 32;      // sequences whose metadata a CTA keeps at hand
 constexpr int kSmallRows = 32; // rows of a block in the SMALL form (one warp's)
 constexpr unsigned FULLMASK = 0xffffffffu;
 
@@ -80,8 +81,9 @@ struct PagedCut {
   int done;    // SMALL: parts finished so far (zero between calls)
   int pad[3];
 };
-// One partial result: O[ROWS][D], then m[ROWS], then l[ROWS]; slot 2b + 1 of
-// CTA b holds a segment that starts there, slot 2b one that started before.
+// One partial result: O as [D / 4][ROWS] groups of 4 values (a thread holds a
+// row, so a warp's stores are whole lines), then m[ROWS], then l[ROWS]; slot
+// 2b + 1 of CTA b holds a segment that starts there, slot 2b one that started before.
 __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<size_t>(ROWS) * (D + 2); }
 
 // A value that every lane of the warp has, as one the compiler may keep in
@@ -109,7 +111,8 @@ struct ACfg {
   static constexpr int STG = SMALL ? 0 : 32 * 128;  // output staging of one softmax warp
   static constexpr int STG_OFF = V_OFF + NV * TILE;
   static constexpr int ML_OFF = STG_OFF + 8 * STG;  // group B's m and l of a shared block (and the schedule's scratch)
-  static constexpr int BAR_OFF = ML_OFF + 2 * BM * 4;
+  static constexpr int SEQ_OFF = ML_OFF + 2 * BM * 4;  // the walk's sequences
+  static constexpr int BAR_OFF = SEQ_OFF + kSeqs * 16;
   // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
   // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, part_full[2], drain[2] (index [2] = tile A / B)
   static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 13;
@@ -122,12 +125,12 @@ struct ACfg {
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { return ROWS >> p.gp_shift; }
 // Virtual units: kPair per key tile of a block with both query tiles, one per
-// key tile of a block with one (measured: 1.9 us and about 1 us), kEnd for a
-// segment's start and end.  A segment is given at least the units of its key
+// key tile of a block with one (measured: 1.8 us and about 1 us), kEnd for a
+// segment's start and end (about 3 us).  A segment is given at least the units of its key
 // tiles, in a form whose sums over a sequence's blocks are closed: off / BN + 1 +
 // ceil((b + 1) tokens / BN) tiles for block b of a sequence with off cells
 // before its new tokens.  All blocks of a sequence but the last have two query tiles.
-constexpr int kPair = 2, kEnd = 1;
+constexpr int kPair = 2, kEnd = 3;
 __device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int b, int weight) {
   return weight * (off / BN + 1 + ((b + 1) * block_tokens(p) + BN - 1) / BN) + kEnd;
 }
@@ -160,8 +163,10 @@ __device__ __forceinline__ int seq_units(const PagedAttentionParams& p, const Pa
 // computes the same prefix sums from the metadata.
 struct Range {
   int v0, v1, w, a, pre;
+  const PagedSeq* seqs;  // sequences a .. a + n_seqs - 1, read once for the CTA
+  int n_seqs;
 };
-__device__ bool find_range(const PagedAttentionParams& p, int* scratch, Range& r) {
+__device__ bool find_range(const PagedAttentionParams& p, int* scratch, PagedSeq* seqs, Range& r) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NW = THREADS / 32;
   // Sums over chunks of one sequence per thread.  The last chunk's prefix stays
@@ -223,6 +228,10 @@ __device__ bool find_range(const PagedAttentionParams& p, int* scratch, Range& r
   __syncthreads();
   r.a = found[0];
   r.pre = found[1];
+  r.seqs = seqs;
+  r.n_seqs = min(kSeqs, p.m.A - r.a);
+  if (tid < r.n_seqs) seqs[tid] = paged_seq(p.m, r.a + tid);
+  __syncthreads();
   return true;
 }
 
@@ -230,6 +239,8 @@ __device__ bool find_range(const PagedAttentionParams& p, int* scratch, Range& r
 // runs its own copy.
 struct PagedWalk {
   const PagedAttentionParams* p;
+  const PagedSeq* seqs;
+  int a_first, n_seqs;
   int v0, v1;
   int a, g, b, nblk;      // segment: sequence, KV head, block of the sequence's nblk
   int first, ql, off;     // the sequence's first packed row, new tokens, cells before them
@@ -240,7 +251,7 @@ struct PagedWalk {
   bool ok;
 
   __device__ __forceinline__ void load_seq() {
-    const PagedSeq s = paged_seq(p->m, a);
+    const PagedSeq s = a - a_first < n_seqs ? seqs[a - a_first] : paged_seq(p->m, a);
     first = s.first;
     ql = s.ql;
     off = s.kl - s.ql;
@@ -276,9 +287,11 @@ struct PagedWalk {
   }
   __device__ void init(const PagedAttentionParams* params, const Range& r) {
     p = params;
+    seqs = r.seqs;
+    a_first = a = r.a;
+    n_seqs = r.n_seqs;
     v0 = r.v0;
     v1 = r.v1;
-    a = r.a;
     load_seq();
     int rem = v0 - r.pre;
     const int head = head_units(*p, ql, off);
@@ -377,7 +390,7 @@ __device__ __forceinline__ void merge_small(const PagedAttentionParams& p, int t
       const float m = __ldcg(s + ROWS * D + row), lb = __ldcg(s + ROWS * D + ROWS + row);
       float4 o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = __ldcg(reinterpret_cast<const float4*>(s + row * D + col) + k);
+      for (int k = 0; k < 4; ++k) o[k] = __ldcg(reinterpret_cast<const float4*>(s) + (col / 4 + k) * ROWS + row);
       if (m == -INFINITY) continue;  // this part saw none of the row's cells
       const float w = exp2f(m - M);
       l += w * lb;
@@ -436,9 +449,11 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     tma_prefetch_map(&map_v);
   }
   pdl_wait();
+  pdl_trigger();  // the next kernel may set itself up on SMs that are done here
   if (threadIdx.x == 0) cut->rows = 0;
   Range range;
-  if (!find_range(p, reinterpret_cast<int*>(smem + C::ML_OFF), range)) return;  // uniform
+  if (!find_range(p, reinterpret_cast<int*>(smem + C::ML_OFF), reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range))
+    return;  // uniform
   PagedWalk walk;
   walk.init(&p, range);
   if (!walk.ok) return;  // uniform: nothing but padding in this range
@@ -854,7 +869,6 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       // 32 values of the row from column q on: the merged accumulators
       auto read_o = [&](int q, uint32_t (&v)[32]) {
         tmem_ld32(o_col + q, v);
-        tmem_wait_ld();
         if (shared) {
           uint32_t w[32];
           tmem_ld32(ob_col + q, w);
@@ -864,6 +878,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
             const float o = wa > 0.f ? __uint_as_float(v[i]) * wa : 0.f;
             v[i] = __float_as_uint(wb > 0.f ? fmaf(__uint_as_float(w[i]), wb, o) : o);
           }
+        } else {
+          tmem_wait_ld();
         }
       };
       auto release_b = [&]() {  // group B's accumulator has been read
@@ -944,7 +960,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
             if (row_ok) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(slot + row * D + q * 32 + k * 4) =
+                *reinterpret_cast<uint4*>(slot + ((q * 8 + k) * ROWS + row) * 4) =
                     make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
           }
@@ -970,50 +986,54 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
 }
 
 // ------------------------------------------------------------------ merge of cut segments
-// CTA (b, y): row group y of the cut segment that starts in CTA b of the
-// attention kernel, one warp per row.  A part whose maximum is -inf saw none
-// of the row's cells and weighs nothing.
+// Warp (b, y): 32 rows and 16 columns of the cut segment that starts in CTA b of
+// the attention kernel, one row to a lane, so that a warp reads whole lines of
+// each part.  A part whose maximum is -inf saw none of the row's cells and
+// weighs nothing.
 constexpr int kMergeWarps = 8;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttentionParams p) {
-  constexpr int VL = D / 32;  // values per lane
   using E = Elem<F16>;
   pdl_wait();
-  const int b0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int task = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int row = task / (D / 16) * 32 + lane, col = task % (D / 16) * 16;
   const PagedCut cut = static_cast<const PagedCut*>(p.cuts)[b0];
-  for (int row = blockIdx.y * kMergeWarps + warp; row < cut.rows; row += gridDim.y * kMergeWarps) {
-    const int gi = row & ((1 << p.gp_shift) - 1);
-    if (gi >= p.G) continue;
-    auto part = [&](int b) { return p.partials + (static_cast<size_t>(b) * 2 + (b == b0)) * slot_floats(D); };
-    float M = -INFINITY;
-    for (int b = b0 + lane; b <= cut.last; b += 32) M = fmaxf(M, part(b)[ROWS * D + row]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULLMASK, M, o));
-    float l = 0.f, acc[VL] = {};
+  const int gi = row & ((1 << p.gp_shift) - 1);
+  if (row >= cut.rows || gi >= p.G) return;
+  auto part = [&](int b) { return p.partials + (static_cast<size_t>(b) * 2 + (b == b0)) * slot_floats(D); };
+  float M = -INFINITY;
 #pragma unroll 4
-    for (int b = b0; b <= cut.last; ++b) {
-      const float* s = part(b);
-      const float m = s[ROWS * D + row], lb = s[ROWS * D + ROWS + row];
-      float o[VL];
-      if constexpr (VL == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(s + row * D + lane * 4);
-      else *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(s + row * D + lane * 2);
-      if (m == -INFINITY) continue;
-      const float w = exp2f(m - M);
-      l += w * lb;
+  for (int b = b0; b <= cut.last; ++b) M = fmaxf(M, part(b)[ROWS * D + row]);
+  float l = 0.f, acc[16] = {};
+#pragma unroll 2
+  for (int b = b0; b <= cut.last; ++b) {
+    const float* s = part(b);
+    const float m = s[ROWS * D + row], lb = s[ROWS * D + ROWS + row];
+    float4 o[4];
 #pragma unroll
-      for (int k = 0; k < VL; ++k) acc[k] += w * o[k];
+    for (int k = 0; k < 4; ++k) o[k] = reinterpret_cast<const float4*>(s)[(col / 4 + k) * ROWS + row];
+    if (m == -INFINITY) continue;
+    const float w = exp2f(m - M);
+    l += w * lb;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[4 * k] += w * o[k].x;
+      acc[4 * k + 1] += w * o[k].y;
+      acc[4 * k + 2] += w * o[k].z;
+      acc[4 * k + 3] += w * o[k].w;
     }
-    const float inv = 1.f / l;
-    const size_t head = static_cast<size_t>(cut.tok + (row >> p.gp_shift)) * p.H_q + cut.g * p.G + gi;
-    uint32_t w[VL / 2];
-#pragma unroll
-    for (int k = 0; k < VL / 2; ++k) w[k] = E::pack2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    uint16_t* dst = p.out + head * D + lane * VL;
-    if constexpr (VL == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(dst) = w[0];
-    if (lane == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.6931471805599453f;
   }
+  const float inv = 1.f / l;
+  const size_t head = static_cast<size_t>(cut.tok + (row >> p.gp_shift)) * p.H_q + cut.g * p.G + gi;
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = E::pack2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + head * D + col);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (col == 0 && p.lse) p.lse[head] = (M + log2f(l)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -1080,9 +1100,10 @@ cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t 
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, paged_attention_kernel<D, F16, SMALL>, p, m.q, m.k, m.v, m.o);
   if (e != cudaSuccess || SMALL) return e;
-  // One row to a warp, as far as the segments' blocks can have them.
+  // As many rows as the segments' blocks can have.
   const int64_t rows = std::min<int64_t>(ROWS, static_cast<int64_t>(p.m.max_query_len) << p.gp_shift);
-  cfg.gridDim = dim3(p.num_ctas, static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps));
+  const int64_t tasks = (rows + 31) / 32 * (D / 16);
+  cfg.gridDim = dim3(p.num_ctas, static_cast<unsigned>((tasks + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F16>, p);

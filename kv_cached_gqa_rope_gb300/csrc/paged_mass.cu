@@ -224,7 +224,12 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   float* lse_s = reinterpret_cast<float*>(smem + C::LSE_OFF);  // [NL][BC]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (warp == W_K && lane == 0) {
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+  }
   pdl_wait();
+  pdl_trigger();  // the next kernel may set itself up on SMs that are done here
   int a0 = 0, pre = 0, v0 = 0, v1 = 0;
   if (!find_start(p, reinterpret_cast<int*>(smem + C::SCR_OFF), a0, pre, v0, v1)) return;  // uniform
   MassWalk walk;
