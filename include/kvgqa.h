@@ -479,7 +479,7 @@ kvgqa_status paged_attention_mass_workspace_size(size_t* bytes);
  * behind every step it gives the weight that each cell has drawn so far, called
  * with a prompt's last tokens the weight of its cells for what comes next; both
  * are what paged_evict_out_ chooses by.  The result does not depend on the run
- * (no atomics).
+ * (every cell is summed in one order and updated once).
  *
  *   q_rot [N,H_q,D], lse [N,H_q] float32, k_cache (read), scale finite
  *   mass [A, H_kv, M] float32 (cells j < kv_lengths[a] of sequences with new

@@ -922,7 +922,21 @@ kvgqa_status paged_rope_kv_store_out_(const kvgqa_tensor* q, const kvgqa_tensor*
     p.status = static_cast<int32_t*>(workspace->data);
     p.H_q = (int)H_q; p.H_kv = (int)H_kv; p.D = (int)D;
     p.f16 = elem == KVGQA_F16;
-    fill_rope_freqs(&p.freqs, (int)D, theta);
+    // The table of this base and width, kept per host thread: evaluating it takes
+    // longer than the rest of the call.
+    struct Table {
+      double theta = 0.0;
+      int64_t D = 0;
+      kvgqa::RopeFreqs freqs{};
+    };
+    thread_local Table table;
+    if (table.D != D || table.theta != theta) {
+      table.D = 0;
+      fill_rope_freqs(&table.freqs, (int)D, theta);
+      table.theta = theta;
+      table.D = D;
+    }
+    p.freqs = table.freqs;
     check_cuda(kvgqa::launch_paged_rope_kv_store(p, static_cast<cudaStream_t>(stream)), "paged_rope_kv_store launch");
   });
 }

@@ -68,7 +68,6 @@ constexpr int kLaunchRegs = 168, kRoleRegs = 72, kSoftmaxRegs = 216;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kRoleRegs <= THREADS * kLaunchRegs, "register split");
 constexpr int TMEM_COLS = 512; // S_A, S_B, O_A, O_B: 128 columns each
 constexpr int UNITS_MIN = 4;   // fewest units a CTA is given
-constexpr int kSeqs = 32;      // sequences whose metadata a CTA keeps at hand
 constexpr int kSmallRows = 32; // rows of a block in the SMALL form (one warp's)
 constexpr unsigned FULLMASK = 0xffffffffu;
 
@@ -85,10 +84,6 @@ struct PagedCut {
 // row, so a warp's stores are whole lines), then m[ROWS], then l[ROWS]; slot
 // 2b + 1 of CTA b holds a segment that starts there, slot 2b one that started before.
 __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<size_t>(ROWS) * (D + 2); }
-
-// A value that every lane of the warp has, as one the compiler may keep in
-// uniform registers (the operands of tcgen05.mma live there).
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(FULLMASK, v, 0); }
 
 // SMALL: no block of the call has more than kSmallRows rows (decode steps, a
 // few tokens per sequence), so the stream of K and V is all there is to it.  The
@@ -112,7 +107,7 @@ struct ACfg {
   static constexpr int STG_OFF = V_OFF + NV * TILE;
   static constexpr int ML_OFF = STG_OFF + 8 * STG;  // group B's m and l of a shared block (and the schedule's scratch)
   static constexpr int SEQ_OFF = ML_OFF + 2 * BM * 4;  // the walk's sequences
-  static constexpr int BAR_OFF = SEQ_OFF + kSeqs * 16;
+  static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * sizeof(PagedSeq);
   // q_full[2], q_empty[2], k_full[NK], k_empty[NK], v_full[NV], v_empty[NV],
   // s_full[2], p_full[2], o_done[2], v_land, ml_full, ml_done, part_full[2], drain[2] (index [2] = tile A / B)
   static constexpr int NBAR = 4 + 2 * NK + 2 * NV + 13;
@@ -158,83 +153,6 @@ __device__ __forceinline__ int seq_units(const PagedAttentionParams& p, const Pa
   return p.H_kv * head_units(p, s.ql, s.kl - s.ql);
 }
 
-// The range [v0, v1) of virtual units of this CTA and the sequence v0 falls
-// in, with that sequence's virtual start.  Called by the whole CTA; every CTA
-// computes the same prefix sums from the metadata.
-struct Range {
-  int v0, v1, w, a, pre;
-  const PagedSeq* seqs;  // sequences a .. a + n_seqs - 1, read once for the CTA
-  int n_seqs;
-};
-__device__ bool find_range(const PagedAttentionParams& p, int* scratch, PagedSeq* seqs, Range& r) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int NW = THREADS / 32;
-  // Sums over chunks of one sequence per thread.  The last chunk's prefix stays
-  // in registers: with no more sequences than threads that is all there is.
-  int before_chunk = 0, units = 0, excl = 0, total = 0;
-  bool bad = false;
-  const int chunks = (p.m.A + THREADS - 1) / THREADS;
-  auto scan = [&](int chunk) {  // exclusive prefix of this thread's sequence, and the total up to the chunk's end
-    const int a = chunk * THREADS + tid;
-    PagedSeq s{};
-    if (a < p.m.A) {
-      s = paged_seq(p.m, a);
-      bad = bad || !s.ok;
-    }
-    units = a < p.m.A ? seq_units(p, s) : 0;
-    int incl = units;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(FULLMASK, incl, o);
-      if (lane >= o) incl += t;
-    }
-    if (chunk > 0) __syncthreads();  // the last chunk's sums have been read
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    before_chunk = total;
-    excl = before_chunk + incl - units;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const int t = scratch[w];
-      if (w < warp) excl += t;
-      total += t;
-    }
-  };
-  for (int c = 0; c < chunks; ++c) scan(c);
-  if (blockIdx.x == 0 && bad) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
-  r.w = max((total + p.num_ctas - 1) / p.num_ctas, UNITS_MIN);
-  // (num_ctas ranges of w units hold the total; a product past 2^31 would mean v0 >= total)
-  const long long v0 = static_cast<long long>(blockIdx.x) * r.w;
-  if (v0 >= total) return false;
-  r.v0 = static_cast<int>(v0);
-  r.v1 = min(r.v0 + r.w, total);
-  int* found = scratch + NW;
-  if (chunks == 1) {
-    if (units > 0 && excl <= r.v0 && r.v0 < excl + units) {
-      found[0] = tid;
-      found[1] = excl;
-    }
-  } else {
-    total = 0;
-    __syncthreads();
-    for (int c = 0; c < chunks; ++c) {
-      scan(c);
-      if (units > 0 && excl <= r.v0 && r.v0 < excl + units) {
-        found[0] = c * THREADS + tid;
-        found[1] = excl;
-      }
-    }
-  }
-  __syncthreads();
-  r.a = found[0];
-  r.pre = found[1];
-  r.seqs = seqs;
-  r.n_seqs = min(kSeqs, p.m.A - r.a);
-  if (tid < r.n_seqs) seqs[tid] = paged_seq(p.m, r.a + tid);
-  __syncthreads();
-  return true;
-}
-
 // Walks the key tiles of this CTA's range, segment by segment; every role
 // runs its own copy.
 struct PagedWalk {
@@ -251,7 +169,7 @@ struct PagedWalk {
   bool ok;
 
   __device__ __forceinline__ void load_seq() {
-    const PagedSeq s = a - a_first < n_seqs ? seqs[a - a_first] : paged_seq(p->m, a);
+    const PagedSeq s = range_seq(p->m, *this, a);
     first = s.first;
     ql = s.ql;
     off = s.kl - s.ql;
@@ -285,7 +203,7 @@ struct PagedWalk {
       if (enter()) return true;
     }
   }
-  __device__ void init(const PagedAttentionParams* params, const Range& r) {
+  __device__ void init(const PagedAttentionParams* params, const PagedRange& r) {
     p = params;
     seqs = r.seqs;
     a_first = a = r.a;
@@ -451,8 +369,10 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
   pdl_wait();
   pdl_trigger();  // the next kernel may set itself up on SMs that are done here
   if (threadIdx.x == 0) cut->rows = 0;
-  Range range;
-  if (!find_range(p, reinterpret_cast<int*>(smem + C::ML_OFF), reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range))
+  PagedRange range;
+  if (!paged_range<THREADS>(p.m, p.status, p.num_ctas, UNITS_MIN, reinterpret_cast<int*>(smem + C::ML_OFF),
+                            reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range,
+                            [&](const PagedSeq& q) { return seq_units(p, q); }))
     return;  // uniform
   PagedWalk walk;
   walk.init(&p, range);

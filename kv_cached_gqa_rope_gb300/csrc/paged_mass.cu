@@ -8,7 +8,7 @@
 // softmax state, no V.  A cell's sum is over queries, so the scores are laid
 // out transposed, S^T = K Q^T with one TMEM lane per cell: each thread adds up
 // one cell's weights in registers, and nothing crosses threads until it writes
-// its cell.  Every cell is summed by one thread in one order (no atomics), so
+// its cell.  Every cell is summed by one thread in one order and updated once, so
 // the result does not depend on how the work is dealt.
 //
 // An item is 256 cells of one sequence and KV head (two 128-cell tiles, A and
@@ -16,11 +16,13 @@
 // with the group padded to a power of two, in blocks of 128.  Per item:
 //   warp 8      TMA of the two K tiles, one box per page (2-stage ring);
 //   warp 9      TMA of the query blocks (ring) and their log sums, as base-2
-//               logs, into shared memory (+inf for columns without a query);
+//               logs, into shared memory (+inf for columns without a query); a
+//               head's blocks stay there for all of its items if they fit the ring;
 //   warp 10     S_x^T = K_x Q^T of each block into TMEM (x = A, B, two buffers each);
 //   warps 0-3   tile A, warps 4-7 tile B: exp2 of the scaled scores less the
 //               column's log sum, added to the cell's sum; at the item's end
-//               each thread updates its cell.
+//               each thread adds that to its cell (as a reduction in L2: a
+//               load would have to be waited for).
 // The items are dealt as contiguous equal shares of their column blocks to a
 // persistent grid.  Single tokens are bound by the stream of K, longer chunks
 // by the exponentials.
@@ -47,6 +49,7 @@ constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub
 constexpr int THREADS = 11 * 32;
 constexpr int W_K = 8, W_Q = 9, W_MMA = 10;
 constexpr int TMEM_COLS = 512; // S^T of A and B, two buffers each, 128 columns
+constexpr int kQueryBlocks = 2; // query blocks in flight, or resident
 constexpr int NL = 8;          // log-sum slots
 constexpr unsigned FULLMASK = 0xffffffffu;
 
@@ -55,13 +58,14 @@ struct MCfg {
   static constexpr int NSUB = D / 64;
   static constexpr int TILE = NSUB * SUB;
   static constexpr int NK = D == 128 ? 2 : 4;       // items in flight
-  static constexpr int NQ = 2;                      // query blocks in flight
+  static constexpr int NQ = kQueryBlocks;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = NK * 2 * TILE;
   static constexpr int LSE_OFF = Q_OFF + NQ * TILE;
   static constexpr int SCR_OFF = LSE_OFF + NL * BC * 4;
   // k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL], s_full[4], s_empty[4], drain
-  static constexpr int BAR_OFF = SCR_OFF + 64 * 4;
+  static constexpr int SEQ_OFF = SCR_OFF + 64 * 4;  // the walk's sequences
+  static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * sizeof(PagedSeq);
   static constexpr int NBAR = 2 * NK + 2 * NQ + 2 * NL + 9;
   static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
@@ -84,13 +88,17 @@ __device__ __forceinline__ int seq_units(const PagedMassParams& p, const PagedSe
 // Walks the items whose first unit lies in this CTA's range.
 struct MassWalk {
   const PagedMassParams* p;
+  const PagedSeq* seqs;
+  int a_first, n_seqs;
+  int loads;              // query blocks loaded for the heads before this one (before this item, if streamed)
+  bool fresh;             // the CTA's first item of this head
   int v, v1;              // the item's first unit, the end of the range
   int a, g, kb;           // sequence, KV head, item of the head
   int first, ql, kl, off, n_items, units, nblk;
   bool ok;
 
   __device__ __forceinline__ void load_seq() {
-    const PagedSeq s = paged_seq(p->m, a);
+    const PagedSeq s = range_seq(p->m, *this, a);
     first = s.first;
     ql = s.ql;
     kl = s.kl;
@@ -100,9 +108,13 @@ struct MassWalk {
     nblk = col_blocks(*p, s);
   }
   __device__ void advance() {
+    if (!resident()) loads += nblk - first_block(0);
+    else if (last()) loads += nblk;
     v += units;
+    fresh = false;
     if (++kb == n_items) {
       kb = 0;
+      fresh = true;
       if (++g == p->H_kv) {
         g = 0;
         do {
@@ -116,14 +128,17 @@ struct MassWalk {
     }
     ok = v < v1;
   }
-  // pre: the first unit of sequence `seq`, which v0 falls in.
-  __device__ void init(const PagedMassParams* params, int seq, int pre, int v0, int end) {
+  __device__ void init(const PagedMassParams* params, const PagedRange& r) {
     p = params;
-    v1 = end;
-    a = seq;
+    seqs = r.seqs;
+    a_first = a = r.a;
+    n_seqs = r.n_seqs;
+    v1 = r.v1;
+    loads = 0;
+    fresh = true;
     load_seq();
-    const int i = (v0 - pre + units - 1) / units;  // the first item from v0 on
-    v = pre + i * units;
+    const int i = (r.v0 - r.pre + units - 1) / units;  // the first item from v0 on
+    v = r.pre + i * units;
     g = i / n_items;
     kb = i % n_items;
     ok = v < v1;
@@ -132,8 +147,13 @@ struct MassWalk {
       kb = n_items - 1;
       v -= units;
       advance();
+      loads = 0;
     }
   }
+  // A head's query blocks stay in the ring for all of its items if they fit;
+  // else every item streams them through it.
+  __device__ __forceinline__ bool resident() const { return nblk <= kQueryBlocks; }
+  __device__ __forceinline__ bool last() const { return kb + 1 == n_items || v + units >= v1; }  // of this head, here
   // Cells of tile x of the item.
   __device__ __forceinline__ int live(int x) const { return min(BK, kl - kb * ITEM - x * BK); }
   __device__ __forceinline__ int tiles() const { return live(1) > 0 ? 2 : 1; }
@@ -144,62 +164,6 @@ struct MassWalk {
     return t <= 0 ? 0 : (t << p->gp_shift) / BC;
   }
 };
-
-// This CTA's range of units and the sequence it begins in; false if there is
-// none.  Every CTA computes the same prefix sums from the metadata.
-__device__ bool find_start(const PagedMassParams& p, int* scratch, int& a0, int& pre, int& v0, int& v1) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int NW = THREADS / 32;
-  int mine = 0, bad = 0;
-  for (int a = tid; a < p.m.A; a += THREADS) {
-    const PagedSeq s = paged_seq(p.m, a);
-    bad |= !s.ok;
-    mine += seq_units(p, s);
-  }
-  if (blockIdx.x == 0 && bad) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(FULLMASK, mine, o);
-  if (lane == 0) scratch[warp] = mine;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) total += scratch[w];
-  const int w = max((total + p.num_ctas - 1) / p.num_ctas, 1);
-  const long long start = static_cast<long long>(blockIdx.x) * w;
-  if (start >= total) return false;
-  v0 = static_cast<int>(start);
-  v1 = min(v0 + w, total);
-  int carry = 0;
-  for (int base = 0; base < p.m.A; base += THREADS) {
-    const int a = base + tid;
-    const int u = a < p.m.A ? seq_units(p, paged_seq(p.m, a)) : 0;
-    int incl = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(FULLMASK, incl, o);
-      if (lane >= o) incl += t;
-    }
-    __syncthreads();
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int before = carry;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const int t = scratch[i];
-      if (i < warp) before += t;
-      carry += t;
-    }
-    const int excl = before + incl - u;
-    if (u > 0 && excl <= v0 && v0 < excl + u) {
-      scratch[NW] = a;
-      scratch[NW + 1] = excl;
-    }
-  }
-  __syncthreads();
-  a0 = scratch[NW];
-  pre = scratch[NW + 1];
-  return true;
-}
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -222,7 +186,7 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SLOT_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::FLAG_OFF);
   float* lse_s = reinterpret_cast<float*>(smem + C::LSE_OFF);  // [NL][BC]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (warp == W_K && lane == 0) {
     tma_prefetch_map(&map_q);
@@ -230,10 +194,13 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   }
   pdl_wait();
   pdl_trigger();  // the next kernel may set itself up on SMs that are done here
-  int a0 = 0, pre = 0, v0 = 0, v1 = 0;
-  if (!find_start(p, reinterpret_cast<int*>(smem + C::SCR_OFF), a0, pre, v0, v1)) return;  // uniform
+  PagedRange range;
+  if (!paged_range<THREADS>(p.m, p.status, p.num_ctas, 1, reinterpret_cast<int*>(smem + C::SCR_OFF),
+                            reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range,
+                            [&](const PagedSeq& q) { return seq_units(p, q); }))
+    return;  // uniform
   MassWalk walk;
-  walk.init(&p, a0, pre, v0, v1);
+  walk.init(&p, range);
   if (!walk.ok) return;  // uniform: no item begins in this range
 
   if (threadIdx.x == 0) {
@@ -264,8 +231,8 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t sbase = smem_u32(smem);
+  const uint32_t tmem = uniform(*tmem_slot);
+  const uint32_t sbase = uniform(smem_u32(smem));
 #define KVGQA_WAIT(bar, parity) __all_sync(FULLMASK, mbar_wait_bounded((bar), (parity), abort_flag, p.status))
 
   if (warp == W_K) {
@@ -308,26 +275,32 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     int n = 0;  // blocks so far
     bool ok = true;
     for (; walk.ok && ok; walk.advance()) {
-      for (int blk = walk.first_block(0); blk < walk.nblk; ++blk, ++n) {
+      if (walk.resident() && !walk.fresh) continue;
+      for (int blk = walk.resident() ? 0 : walk.first_block(0); blk < walk.nblk; ++blk, ++n) {
         const int tok0 = (blk * BC) >> p.gp_shift;
-        // log sums of this lane's 4 columns, in base 2 (loaded before the wait)
-        float ls[BC / 32];
-#pragma unroll
-        for (int i = 0; i < BC / 32; ++i) {
-          const int col = lane + 32 * i, t = tok0 + (col >> p.gp_shift), h = col & (gp - 1);
-          ls[i] = INFINITY;
-          if (t < walk.ql && h < p.G)
-            ls[i] = p.lse[static_cast<size_t>(walk.first + t) * p.H_q + walk.g * p.G + h] * 1.4426950408889634f;
-        }
         const int s = n % C::NQ;
-        ok = (n < C::NQ || KVGQA_WAIT(&q_empty[s], ((n / C::NQ) - 1) & 1)) &&
-             (n < NL || KVGQA_WAIT(&l_empty[n % NL], ((n / NL) - 1) & 1));
+        ok = n < C::NQ || KVGQA_WAIT(&q_empty[s], ((n / C::NQ) - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&q_full[s], p.box_tokens * gp * 128 * C::NSUB);
           for (int sub = 0; sub < C::NSUB; ++sub)
             tma_load_4d(smem + C::Q_OFF + s * C::TILE + sub * SUB, &map_q, sub * 64, 0, walk.g, walk.first + tok0,
                         &q_full[s], pol);
+        }
+        __syncwarp();
+        // log sums of this lane's 4 columns, in base 2 and negated
+        float ls[BC / 32];
+#pragma unroll
+        for (int i = 0; i < BC / 32; ++i) {
+          const int col = lane + 32 * i, t = tok0 + (col >> p.gp_shift), h = col & (gp - 1);
+          ls[i] = -INFINITY;
+          if (t < walk.ql && h < p.G)
+            ls[i] = p.lse[static_cast<size_t>(walk.first + t) * p.H_q + walk.g * p.G + h] * -1.4426950408889634f;
+        }
+        ok = n < NL || KVGQA_WAIT(&l_empty[n % NL], ((n / NL) - 1) & 1);
+        if (!ok) {
+          ++n;  // (its query block is on the way)
+          break;
         }
 #pragma unroll
         for (int i = 0; i < BC / 32; ++i) lse_s[(n % NL) * BC + lane + 32 * i] = ls[i];
@@ -343,19 +316,23 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     }
   } else if (warp == W_MMA) {
     // ------------------------------------------------------------ MMA issuer
-    int it = 0, n = 0, sn[2] = {0, 0};
+    int it = 0, sn[2] = {0, 0};
     bool ok = true, issued = false;
     for (; walk.ok && ok; walk.advance(), ++it) {
       const int ks = it % C::NK;
+      const bool resident = walk.resident();
       if (!KVGQA_WAIT(&k_full[ks], (it / C::NK) & 1)) break;
       const int fb0 = walk.first_block(0), fb1 = walk.first_block(1), tiles = walk.tiles();
-      for (int blk = fb0; blk < walk.nblk; ++blk, ++n) {
-        const int qs = n % C::NQ;
-        ok = KVGQA_WAIT(&q_full[qs], (n / C::NQ) & 1);
+      if (resident && walk.fresh)
+        for (int n = walk.loads; n < walk.loads + walk.nblk && ok; ++n) ok = KVGQA_WAIT(&q_full[n % C::NQ], (n / C::NQ) & 1);
+      if (!ok) break;
+      for (int blk = fb0; blk < walk.nblk; ++blk) {
+        const int n = walk.loads + (resident ? blk : blk - fb0), qs = n % C::NQ;
+        if (!resident) ok = KVGQA_WAIT(&q_full[qs], (n / C::NQ) & 1);
         if (!ok) break;
         // only the columns that hold a query, in whole groups of 16
         const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
-        const uint32_t idesc = idesc_f16kind_f32(E::kMmaFormat, BK, (cols + 15) & ~15, 0);
+        const uint32_t idesc = uniform(idesc_f16kind_f32(E::kMmaFormat, BK, (cols + 15) & ~15, 0));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (x == 1 && (tiles < 2 || blk < fb1)) continue;
@@ -366,14 +343,14 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
           }
           ++sn[x];
           tc_fence_after();
-          const uint32_t k_addr = sbase + C::K_OFF + (ks * 2 + x) * C::TILE;
-          const uint32_t q_addr = sbase + C::Q_OFF + qs * C::TILE;
+          const uint32_t k_lo = smem_desc_lo(sbase + C::K_OFF + (ks * 2 + x) * C::TILE, 16);
+          const uint32_t q_lo = smem_desc_lo(uniform(sbase + C::Q_OFF + qs * C::TILE), 16);
+          const uint32_t s_tm = uniform(tmem + buf * BC);
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = (kk / 4) * SUB + (kk % 4) * 32;
-              umma_f16_ss(tmem + buf * BC, smem_desc_sw128(k_addr + o, 16, 1024), smem_desc_sw128(q_addr + o, 16, 1024),
-                          idesc, kk > 0);
+              const uint32_t o = (kk / 4) * (SUB >> 4) + (kk % 4) * (32 >> 4);
+              umma_f16_ss_lo(s_tm, k_lo + o, q_lo + o, idesc, kk > 0);
             }
             umma_commit(&s_full[buf]);
           }
@@ -381,11 +358,17 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
           issued = true;
         }
         if (!ok) break;
-        if (elect_one()) umma_commit(&q_empty[qs]);
-        __syncwarp();
+        if (!resident) {
+          if (elect_one()) umma_commit(&q_empty[qs]);
+          __syncwarp();
+        }
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&k_empty[ks]);
+      if (elect_one()) {
+        umma_commit(&k_empty[ks]);
+        if (resident && walk.last())
+          for (int n = walk.loads; n < walk.loads + walk.nblk; ++n) umma_commit(&q_empty[n % C::NQ]);
+      }
       __syncwarp();
     }
     if (*abort_flag && issued) {
@@ -400,65 +383,100 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     const int r = threadIdx.x & 127;   // cell of the tile == TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-    int n = 0, sn = 0;  // column blocks of the CTA, and those of this tile
+    int sn = 0;  // column blocks of this tile so far
     bool ok = true;
+    // The log sums of load n are there; they are done with.
+    auto take = [&](int n) {
+      ok = ok && __all_sync(FULLMASK, mbar_wait_bounded(&l_full[n % NL], (n / NL) & 1, abort_flag, p.status));
+    };
+    auto pass = [&](int n) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&l_empty[n % NL]);
+    };
     for (; walk.ok && ok; walk.advance()) {
-      const int live = walk.live(x);
-      // Blocks that this tile does not use: their log sums are passed on.
+      const int live = walk.live(x), fb0 = walk.first_block(0);
+      const bool resident = walk.resident();
+      if (resident && walk.fresh)
+        for (int n = walk.loads; n < walk.loads + walk.nblk; ++n) take(n);
+      // Streamed blocks that this tile does not use are passed on.
       const int fb = live > 0 ? walk.first_block(x) : walk.nblk;
-      for (int blk = walk.first_block(0); blk < fb && ok; ++blk, ++n) {
-        ok = __all_sync(FULLMASK, mbar_wait_bounded(&l_full[n % NL], (n / NL) & 1, abort_flag, p.status));
-        if (lane == 0) mbar_arrive(&l_empty[n % NL]);
-      }
+      if (!resident)
+        for (int n = walk.loads; n < walk.loads + fb - fb0 && ok; ++n) {
+          take(n);
+          pass(n);
+        }
       if (!ok) break;
-      if (live <= 0) continue;  // the item has no tile B
-      const int cell = walk.kb * ITEM + x * BK + r;
-      float* dst = p.mass + (static_cast<size_t>(walk.a) * p.H_kv + walk.g) * p.mass_cells + cell;
-      const float before = r < live ? *dst : 0.f;
-      // column i of block blk sees this cell iff blk * BC + i >= c_min
-      const int c_min = max(cell - walk.off, 0) << p.gp_shift;
-      const int c_tile = max(walk.kb * ITEM + x * BK + live - 1 - walk.off, 0) << p.gp_shift;  // the tile's largest
-      float2 sum = make_float2(0.f, 0.f);
-      for (int blk = fb; blk < walk.nblk; ++blk, ++n, ++sn) {
-        const int buf = x * 2 + (sn & 1);
-        ok = __all_sync(FULLMASK, mbar_wait_bounded(&s_full[buf], (sn >> 1) & 1, abort_flag, p.status));
-        if (ok) ok = __all_sync(FULLMASK, mbar_wait_bounded(&l_full[n % NL], (n / NL) & 1, abort_flag, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        const float* ls = lse_s + (n % NL) * BC;
-        const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
-        const bool band = blk * BC < c_tile;
-        const int lo = c_min - blk * BC;
-#pragma unroll 1
-        for (int q = 0; q < cols; q += 32) {
-          uint32_t u[32];
-          tmem_ld32(tmem + lane_base + buf * BC + q, u);
-          tmem_wait_ld();
-          float* sv = reinterpret_cast<float*>(u);
-          if (band || q + 32 > cols) {  // columns that do not see the cell, or hold no query
+      if (live > 0) {
+        const int cell = walk.kb * ITEM + x * BK + r;
+        float* dst = p.mass + (static_cast<size_t>(walk.a) * p.H_kv + walk.g) * p.mass_cells + cell;
+        // column i of block blk sees this cell iff blk * BC + i >= c_min
+        const int c_min = max(cell - walk.off, 0) << p.gp_shift;
+        const int c_tile = max(walk.kb * ITEM + x * BK + live - 1 - walk.off, 0) << p.gp_shift;  // the tile's largest
+        float2 sum = make_float2(0.f, 0.f);
+        for (int blk = fb; blk < walk.nblk; ++blk, ++sn) {
+          const int buf = x * 2 + (sn & 1), n = walk.loads + (resident ? blk : blk - fb0);
+          ok = __all_sync(FULLMASK, mbar_wait_bounded(&s_full[buf], (sn >> 1) & 1, abort_flag, p.status));
+          if (!resident) take(n);
+          if (!ok) break;
+          tc_fence_after();
+          const float* ls = lse_s + (n % NL) * BC;
+          const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
+          const uint32_t s_tm = tmem + lane_base + buf * BC;
+          // 32 columns at a time, the next read while the weights of one lot are
+          // computed.  In a block at a sequence's end, or over cells that some of
+          // its tokens do not see, columns are picked one by one.
+          const bool picked = blk * BC < c_tile;
+          const int lo = c_min - blk * BC;
+          float2 sum1 = make_float2(0.f, 0.f);
+          if (cols <= 16) {  // single tokens: their heads alone
+            uint32_t u[16];
+            tmem_ld16(s_tm, u);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              sum.x += q + i >= lo && q + i < cols ? ex2(fmaf(sv[i], p.scale_log2, -ls[q + i])) : 0.f;
+            for (int i = 0; i < 16; ++i) {
+              const float w = ex2(fmaf(__uint_as_float(u[i]), p.scale_log2, ls[i]));
+              sum.x += i >= lo && i < cols ? w : 0.f;
+            }
           } else {
+            uint32_t u[2][32];
+            tmem_ld32(s_tm, u[0]);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(ls + q + i);
-              const float2 xa = ffma2(make_float2(sv[i], sv[i + 1]), c2, make_float2(-l4.x, -l4.y));
-              const float2 xb = ffma2(make_float2(sv[i + 2], sv[i + 3]), c2, make_float2(-l4.z, -l4.w));
-              sum = fadd2(sum, make_float2(ex2(xa.x), ex2(xa.y)));
-              sum = fadd2(sum, make_float2(ex2(xb.x), ex2(xb.y)));
+            for (int q = 0; q < BC; q += 32) {
+              if (q < cols) {  // uniform
+                tmem_wait_ld();
+                if (q + 32 < BC) tmem_ld32(s_tm + q + 32, u[(q / 32 + 1) & 1]);
+                const float* sv = reinterpret_cast<const float*>(u[(q / 32) & 1]);
+                if (!picked && q + 32 <= cols) {
+#pragma unroll
+                  for (int i = 0; i < 32; i += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(ls + q + i);
+                    const float2 xa = ffma2(make_float2(sv[i], sv[i + 1]), c2, make_float2(l4.x, l4.y));
+                    const float2 xb = ffma2(make_float2(sv[i + 2], sv[i + 3]), c2, make_float2(l4.z, l4.w));
+                    sum = fadd2(sum, make_float2(ex2(xa.x), ex2(xa.y)));
+                    sum1 = fadd2(sum1, make_float2(ex2(xb.x), ex2(xb.y)));
+                  }
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const float w = ex2(fmaf(sv[i], p.scale_log2, ls[q + i]));
+                    sum.x += q + i >= lo && q + i < cols ? w : 0.f;
+                  }
+                }
+              }
             }
           }
+          tmem_wait_ld();  // (the read ahead of a short block's last lot)
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[buf]);
+          sum = fadd2(sum, sum1);
+          if (!resident) pass(n);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_empty[buf]);
-          mbar_arrive(&l_empty[n % NL]);
-        }
+        if (!ok) break;
+        if (r < live) atomicAdd(dst, sum.x + sum.y);  // the cell's only update in this call: nothing to wait for
       }
-      if (!ok) break;
-      if (r < live) *dst = before + (sum.x + sum.y);
+      if (resident && walk.last())
+        for (int n = walk.loads; n < walk.loads + walk.nblk; ++n) pass(n);
     }
   }
 #undef KVGQA_WAIT

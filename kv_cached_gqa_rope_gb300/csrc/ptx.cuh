@@ -158,6 +158,10 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// A value that every lane of the warp has, as one the compiler may keep in
+// uniform registers (the operands of tcgen05.mma live there).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // One lane of a converged warp (the same one every lane agrees on).
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
@@ -194,28 +198,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// 2^x of two numbers on the FMA pipe, which leaves the special-function unit
-// (16 results per SM and clock) to the others: x = n + f with n the nearest
-// integer (adding 1.5 * 2^23 leaves n in the low bits), 2^f by the degree-5
-// polynomial of least relative error on [-1/2, 1/2] (7.5e-8; evaluated in FP32
-// 2.2e-7), n added to the exponent.  x is clamped to -126 from below, where
-// ex2 gives zero, and must stay below 127; -inf gives 2^-126, not zero.
-__device__ __forceinline__ float2 ex2_fma2(float2 x) {
-  x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
-  const float2 magic = make_float2(12582912.f, 12582912.f), unmagic = make_float2(-12582912.f, -12582912.f);
-  const float2 t = fadd2(x, magic);
-  const float2 n = fadd2(t, unmagic);
-  const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);
-  float2 r = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
-  r = ffma2(r, f, make_float2(9.675540961325169e-3f, 9.675540961325169e-3f));
-  r = ffma2(r, f, make_float2(5.550713092088699e-2f, 5.550713092088699e-2f));
-  r = ffma2(r, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
-  r = ffma2(r, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
-  r = ffma2(r, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
-  return make_float2(__uint_as_float(__float_as_uint(r.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(r.y) + (__float_as_uint(t.y) << 23)));
 }
 
 }  // namespace kvgqa
