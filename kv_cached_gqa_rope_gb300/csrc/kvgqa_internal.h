@@ -167,7 +167,9 @@ struct PagedAttentionParams {
   PagedMeta m;
   int H_q, H_kv, G, D, f16, num_ctas;
   int out_32b;                  // out is 32-byte aligned (set by the launcher)
-  int gp_shift, box_tokens;     // log2 of the group size padded to a power of two, tokens of a query box (set by the launcher)
+  // Set by the launcher: log2 of the group size padded to a power of two, the
+  // tokens of a query box, and the schedule's cost of a segment's end.
+  int gp_shift, box_tokens, end_units;
   float scale_log2;             // scale * log2(e)
 };
 // Workspace of the paged attention behind the status block.

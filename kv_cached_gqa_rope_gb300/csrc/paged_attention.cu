@@ -120,16 +120,25 @@ struct ACfg {
 // ------------------------------------------------------------------ schedule
 __device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { return ROWS >> p.gp_shift; }
 // Virtual units: kPair per key tile of a block with both query tiles, one per
-// key tile of a block with one (measured: 1.8 us and about 1 us), kEnd for a
-// segment's start and end (about 3 us).  A segment is given at least the units of its key
-// tiles, in a form whose sums over a sequence's blocks are closed: off / BN + 1 +
-// ceil((b + 1) tokens / BN) tiles for block b of a sequence with off cells
-// before its new tokens.  All blocks of a sequence but the last have two query tiles.
-constexpr int kPair = 2, kEnd = 3;
-__device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int b, int weight) {
-  return weight * (off / BN + 1 + ((b + 1) * block_tokens(p) + BN - 1) / BN) + kEnd;
+// key tile of a block with one, p.end_units for a segment's start and end
+// (measured per CTA of a mixed step: 1.67, 1.0 and 3.7 us; of a small call,
+// where the stream of K and V is the bound: 1.25 and 1.9 us).  A sequence's last
+// block counts its key tiles; the others, all with two query tiles, count
+// off / BN + 1 + ceil((b + 1) tokens / BN) of them, at least what they have, for
+// off cells before the new tokens: a form whose sums over blocks are closed.  A
+// segment counts at least the fewest units of a CTA, so that few short ones are
+// dealt whole, one to a CTA (4 of up to 500 cells: 10.2 us, cut finer 12.4).
+constexpr int kPair = 2;
+__device__ __forceinline__ int block_weight(const PagedAttentionParams& p, int ql, int b) {
+  return (ql - b * block_tokens(p)) << p.gp_shift > BM ? kPair : 1;
 }
-// The units of a sequence's first n blocks, all of them pairs.
+// The units of block b of a sequence with ql new tokens.
+__device__ __forceinline__ int seg_units(const PagedAttentionParams& p, int off, int ql, int b) {
+  const int end = (b + 1) * block_tokens(p);
+  return end < ql ? kPair * (off / BN + 1 + (end + BN - 1) / BN) + p.end_units
+                  : max(block_weight(p, ql, b) * ((off + ql + BN - 1) / BN) + p.end_units, UNITS_MIN);
+}
+// The units of a sequence's first n blocks, none of them its last.
 __device__ __forceinline__ int pair_units(const PagedAttentionParams& p, int off, int n) {
   int s;  // the sum of ceil(i tokens / BN) over i = 1 .. n
   if (p.gp_shift == 0) {
@@ -138,16 +147,13 @@ __device__ __forceinline__ int pair_units(const PagedAttentionParams& p, int off
     const int sh = p.gp_shift - 1, m = n >> sh, r = n & ((1 << sh) - 1);
     s = ((m * (m + 1)) >> 1 << sh) + r * (m + 1);  // 2^sh blocks to a key tile: ceil(i / 2^sh)
   }
-  return kPair * (n * (off / BN + 1) + s) + kEnd * n;
-}
-__device__ __forceinline__ int block_weight(const PagedAttentionParams& p, int ql, int b) {
-  return (ql - b * block_tokens(p)) << p.gp_shift > BM ? kPair : 1;
+  return kPair * (n * (off / BN + 1) + s) + p.end_units * n;
 }
 // The units of one KV head of a sequence.
 __device__ __forceinline__ int head_units(const PagedAttentionParams& p, int ql, int off) {
   if (ql == 0) return 0;
   const int b = (ql - 1) / block_tokens(p);  // the last block
-  return pair_units(p, off, b) + seg_units(p, off, b, block_weight(p, ql, b));
+  return pair_units(p, off, b) + seg_units(p, off, ql, b);
 }
 __device__ __forceinline__ int seq_units(const PagedAttentionParams& p, const PagedSeq& s) {
   return p.H_kv * head_units(p, s.ql, s.kl - s.ql);
@@ -188,7 +194,7 @@ struct PagedWalk {
   }
   __device__ bool next_segment() {
     for (;;) {
-      vlo += seg_units(*p, off, b, weight);
+      vlo += seg_units(*p, off, ql, b);
       if (vlo >= v1) return false;
       if (++b == nblk) {
         b = 0;
@@ -1029,10 +1035,13 @@ cudaError_t launch_d(const PagedAttentionParams& p, const Maps& m, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, F16>, p);
 }
 
+bool is_small(const PagedAttentionParams& p) {
+  return static_cast<int64_t>(p.m.max_query_len) << p.gp_shift <= kSmallRows;
+}
+
 template <int D>
 cudaError_t launch_width(const PagedAttentionParams& p, const Maps& m, cudaStream_t stream) {
-  if (static_cast<int64_t>(p.m.max_query_len) << p.gp_shift <= kSmallRows)
-    return p.f16 ? launch_d<D, true, true>(p, m, stream) : launch_d<D, false, true>(p, m, stream);
+  if (is_small(p)) return p.f16 ? launch_d<D, true, true>(p, m, stream) : launch_d<D, false, true>(p, m, stream);
   return p.f16 ? launch_d<D, true, false>(p, m, stream) : launch_d<D, false, false>(p, m, stream);
 }
 
@@ -1064,6 +1073,7 @@ cudaError_t launch_paged_attention(const PagedAttentionParams& params, cudaStrea
   // are whatever the buffer held, which no other row sees.
   p.box_tokens = 1;
   while (p.box_tokens << p.gp_shift < BM && p.box_tokens < p.m.max_query_len) p.box_tokens *= 2;
+  p.end_units = is_small(p) ? 2 : 4;
   Maps m;
   const cudaError_t e = make_maps(p, &m);
   if (e != cudaSuccess) return e;
