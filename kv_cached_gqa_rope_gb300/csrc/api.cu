@@ -381,6 +381,7 @@ kvgqa_status cached_gqa_attention_out_(const kvgqa_tensor* q_rot, const kvgqa_te
     View vp = check_tensor("positions", positions, 1, KVGQA_I32, 4);
     View vr = check_tensor("cache_rows", cache_rows, 1, KVGQA_I32, 4);
     View vo = check_tensor("out", out, 3, elem, 16);
+    require_shape(vkc, {S, H_kv, max_seq, D});
     require_shape(vvc, {S, H_kv, max_seq, D});
     require_shape(vp, {A});
     require_shape(vr, {A});
@@ -472,6 +473,7 @@ void decode_step_body(const kvgqa_tensor* q, const kvgqa_tensor* k, const kvgqa_
     require_shape(vv, {A, H_kv, D});
     require_shape(vp, {A});
     require_shape(vr, {A});
+    require_shape(vkc, {S, H_kv, max_seq, D});
     require_shape(vvc, {S, H_kv, max_seq, D});
     require_shape(vo, {A, H_q, D});
     View vws0 = check_workspace(workspace, KVGQA_STATUS_BYTES);
@@ -592,6 +594,7 @@ kvgqa_status cached_gqa_attention_static_scratch_out_(const kvgqa_tensor* q_rot,
     View vp = check_tensor("positions", positions, 1, KVGQA_I32, 4);
     View vr = check_tensor("cache_rows", cache_rows, 1, KVGQA_I32, 4);
     View vo = check_tensor("out", out, 3, elem, 16);
+    require_shape(vkc, {S, H_kv, max_seq, D});
     require_shape(vvc, {S, H_kv, max_seq, D});
     require_shape(vp, {A});
     require_shape(vr, {A});
@@ -678,6 +681,7 @@ void prefill_body(const kvgqa_tensor* q, const kvgqa_tensor* k, const kvgqa_tens
   require_shape(vk, {A, T, H_kv, D});
   require_shape(vv, {A, T, H_kv, D});
   require_shape(vr, {A});
+  require_shape(vkc, {S, H_kv, max_seq, D});
   require_shape(vvc, {S, H_kv, max_seq, D});
   require_shape(vo, {A, T, H_q, D});
   View voff{}, vlen{};
