@@ -467,7 +467,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillParams p, const __grid_c
       if (grow) {
         alpha = first ? 0.f : ex2(m_ref - mt);
         m_ref = mt;
-        l *= alpha;
+        l = first ? 0.f : l * alpha;  // (the last item's row may have been padding, its sum anything)
       }
       // S_x of this tile being ready means the P.V of the previous tile is
       // complete, so O_x may be rescaled here without a further wait.
