@@ -14,6 +14,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 #include <string>
 
 #include "kvgqa.h"
@@ -119,7 +120,7 @@ View check_tensor(const char* name, const kvgqa_tensor* t, int ndim, int32_t dty
     if (__builtin_mul_overflow(bytes, t->shape[i], &bytes))
       fail(KVGQA_EINVAL, "%s: sizes overflow a 64-bit byte count", name);
   int64_t expect = 1;
-  for (int i = ndim - 1; i >= 0; --i) {
+  for (int i = ndim - 1; i >= 0 && !empty; --i) {  // (the strides of a tensor without elements say nothing)
     if (t->shape[i] > 1 && t->strides[i] != expect)
       fail(KVGQA_ELAYOUT, "%s: not contiguous row-major (dim %d stride %lld, expected %lld)", name,
            i, (long long)t->strides[i], (long long)expect);
@@ -147,6 +148,33 @@ int32_t storage_type(const kvgqa_tensor* t, const char* name) {
   return t->dtype;
 }
 
+// cuPointerGetAttributes from the driver (looked up once); nullptr if absent.
+PFN_cuPointerGetAttributes_v7000 pointer_query() {
+  static PFN_cuPointerGetAttributes_v7000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &f, 7000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuPointerGetAttributes_v7000>(f);
+  });
+  return fn;
+}
+
+// Whether the driver knows the pointer as plain device memory of `device` (the
+// usual case, answered in a fraction of the runtime's query).
+bool plain_device_memory(const void* ptr, int device) {
+  const auto query = pointer_query();
+  if (!query) return false;
+  unsigned type = 0;
+  int ordinal = -1;
+  CUpointer_attribute which[2] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL};
+  void* out[2] = {&type, &ordinal};
+  return query(2, which, out, reinterpret_cast<CUdeviceptr>(ptr)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE &&
+         ordinal == device;
+}
+
 // The device checks: the declared device is the current one, and CUDA knows
 // the pointer as device (or managed) memory of that device.
 void check_device(std::initializer_list<const View*> views, int device) {
@@ -155,6 +183,7 @@ void check_device(std::initializer_list<const View*> views, int device) {
     const kvgqa_tensor* t = v->t;
     if (t->device != device)
       fail(KVGQA_EDEVICE, "%s: on device %d, current device is %d", v->name, t->device, device);
+    if (plain_device_memory(t->data, device)) continue;
     cudaPointerAttributes attr;
     if (cudaPointerGetAttributes(&attr, t->data) != cudaSuccess) {
       cudaGetLastError();

@@ -43,14 +43,15 @@ __device__ __forceinline__ int paged_page(const PagedMeta& m, int a, int cell) {
 // planning kernel and no plan to keep.
 struct PagedRange {
   int v0, v1, w, a, pre;
-  const PagedSeq* seqs;  // sequences a .. a + n_seqs - 1, read once for the CTA
-  int n_seqs;
+  const PagedSeq* seqs;  // sequences first_seq .. + n_seqs - 1, read once for the CTA
+  int first_seq, n_seqs;
 };
 constexpr int kPagedSeqs = 32;  // sequences whose metadata a CTA keeps at hand
 
 // Called by the whole CTA of THREADS; units(seq) gives a sequence's units (their
 // sum below 2^30), scratch has THREADS / 32 + 2 ints and seqs kPagedSeqs entries
-// of shared memory.  False if nothing is left for this CTA.
+// of shared memory.  False if nothing is left for this CTA.  Passes a barrier of
+// the CTA in either case (m.A > 0).
 template <int THREADS, typename Units>
 __device__ bool paged_range(const PagedMeta& m, int32_t* status, int num_ctas, int min_units, int* scratch,
                             PagedSeq* seqs, PagedRange& r, Units units_of) {
@@ -68,6 +69,7 @@ __device__ bool paged_range(const PagedMeta& m, int32_t* status, int num_ctas, i
       const PagedSeq s = paged_seq(m, a);
       bad = bad || !s.ok;
       units = units_of(s);
+      if (m.A <= kPagedSeqs) seqs[a] = s;
     }
     int incl = units;
 #pragma unroll
@@ -114,9 +116,14 @@ __device__ bool paged_range(const PagedMeta& m, int32_t* status, int num_ctas, i
   r.a = found[0];
   r.pre = found[1];
   r.seqs = seqs;
-  r.n_seqs = min(kPagedSeqs, m.A - r.a);
-  if (tid < r.n_seqs) seqs[tid] = paged_seq(m, r.a + tid);
-  __syncthreads();
+  r.first_seq = 0;
+  r.n_seqs = m.A;
+  if (m.A > kPagedSeqs) {  // the table holds the first of this CTA's
+    r.first_seq = r.a;
+    r.n_seqs = min(kPagedSeqs, m.A - r.a);
+    if (tid < r.n_seqs) seqs[tid] = paged_seq(m, r.a + tid);
+    __syncthreads();
+  }
   return true;
 }
 

@@ -131,7 +131,8 @@ struct MassWalk {
   __device__ void init(const PagedMassParams* params, const PagedRange& r) {
     p = params;
     seqs = r.seqs;
-    a_first = a = r.a;
+    a = r.a;
+    a_first = r.first_seq;
     n_seqs = r.n_seqs;
     v1 = r.v1;
     loads = 0;
@@ -188,21 +189,11 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   float* lse_s = reinterpret_cast<float*>(smem + C::LSE_OFF);  // [NL][BC]
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
+  // What needs no input comes before the wait for the previous kernel.
   if (warp == W_K && lane == 0) {
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
   }
-  pdl_wait();
-  pdl_trigger();  // the next kernel may set itself up on SMs that are done here
-  PagedRange range;
-  if (!paged_range<THREADS>(p.m, p.status, p.num_ctas, 1, reinterpret_cast<int*>(smem + C::SCR_OFF),
-                            reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range,
-                            [&](const PagedSeq& q) { return seq_units(p, q); }))
-    return;  // uniform
-  MassWalk walk;
-  walk.init(&p, range);
-  if (!walk.ok) return;  // uniform: no item begins in this range
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(&k_full[s], 1);
@@ -229,8 +220,22 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();  // the next kernel may set itself up on SMs that are done here
+  PagedRange range;
+  bool work = paged_range<THREADS>(p.m, p.status, p.num_ctas, 1, reinterpret_cast<int*>(smem + C::SCR_OFF),
+                                   reinterpret_cast<PagedSeq*>(smem + C::SEQ_OFF), range,
+                                   [&](const PagedSeq& q) { return seq_units(p, q); });
+  tc_fence_after();  // (past the barriers of paged_range)
+  MassWalk walk;
+  if (work) {
+    walk.init(&p, range);
+    work = walk.ok;
+  }
+  if (!work) {  // uniform: no item begins in this range
+    if (warp == W_MMA) tmem_dealloc(*tmem_slot, TMEM_COLS);
+    return;
+  }
   const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t sbase = uniform(smem_u32(smem));
 #define KVGQA_WAIT(bar, parity) __all_sync(FULLMASK, mbar_wait_bounded((bar), (parity), abort_flag, p.status))

@@ -197,6 +197,8 @@ def test_rows_of_no_sequence_and_no_rows():
         p = Paged([0] * A, [5] * A, 4, 2, 64, 16, BF, seed=107, behind=behind).cuda()
         out, _, flags = attend(p)
         assert flags == 0 and torch.all(out == 7.0)
+        _, flags = store(p, torch.zeros(3, p.N, dtype=torch.int32).cuda(), [0] * 32)
+        assert flags == 0
 
 
 def test_evict_many_sequences_at_the_border():

@@ -183,6 +183,19 @@ def test_evict_refusals():
         assert e.value.code == "EINVAL"
 
 
+def test_empty_operands_of_any_stride_are_taken():
+    """A call without tokens, as torch strides its tensors."""
+    m = dict(query_starts=torch.zeros(3, dtype=I32), kv_lengths=torch.full((2,), 20, dtype=I32),
+             block_table=torch.zeros(2, 2, dtype=I32))
+    assert code_of(kv.paged_rope_kv_store_out_, **dict(store_args(N=0), **m)) in PAST_THE_CHECKS
+    assert code_of(kv.paged_gqa_attention_out_, **dict(attention_args(N=0), **m)) in PAST_THE_CHECKS
+    assert code_of(kv.paged_attention_mass_out_, **dict(mass_args(N=0), **m)) in PAST_THE_CHECKS
+    m["block_table"] = torch.zeros(2, 0, dtype=I32)               # and a table without pages
+    assert code_of(kv.paged_attention_mass_out_, **dict(mass_args(N=0), **m)) in PAST_THE_CHECKS
+    a = evict_args(mass=torch.zeros(2, 2, 0), mass_out=torch.zeros(2, 2, 0), block_table=m["block_table"])
+    assert code_of(kv.paged_evict_out_, **a) in PAST_THE_CHECKS
+
+
 def test_workspace_sizes():
     assert kv.paged_rope_kv_store_workspace_size() == 256
     assert kv.paged_attention_mass_workspace_size() == 256
