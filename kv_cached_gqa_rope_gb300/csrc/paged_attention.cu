@@ -50,6 +50,7 @@
 
 #include "elem.cuh"
 #include "paged.cuh"
+#include "paged_tiles.cuh"
 #include "tcgen05.cuh"
 
 namespace kvgqa {
@@ -58,7 +59,7 @@ namespace {
 constexpr int BM = 128;        // rows of a query tile
 constexpr int BN = 128;        // keys of a tile
 constexpr int ROWS = 2 * BM;   // rows of a segment's block: tiles A and B
-constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
+constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile of a query tile
 constexpr int THREADS = 12 * 32;
 constexpr int W_K = 8, W_V = 9, W_MMA = 10;  // and W_MMA + 1
 // Register split (setmaxnreg): the launch gives every thread kLaunchRegs; the
@@ -94,7 +95,8 @@ __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<siz
 template <int D, bool SMALL>
 struct ACfg {
   static constexpr int NSUB = D / 64;
-  static constexpr int TILE = NSUB * SUB;           // one K or V tile
+  using Tile = PagedTile<D>;
+  static constexpr int TILE = Tile::BYTES;          // one K or V tile
   static constexpr int QSUB = SMALL ? kSmallRows * 128 : SUB;
   static constexpr int QTILE = NSUB * QSUB;         // one query tile
   static constexpr int NK = 2 * 128 / D;            // K stages
@@ -262,26 +264,31 @@ struct PagedWalk {
   }
 };
 
-// The TMA boxes of the walk's K or V tile: lane i < boxes() takes the cells
-// from j * BN + i * box_rows on.
+// The TMA boxes of the walk's K or V tile: lane i < n takes the cells from
+// j * BN + i * rows on.  A lane's table entry is read one tile ahead within a
+// segment: its latency (700 clocks) would stand before every tile's copy.
 struct TileBoxes {
-  int n, rows, c1, c2;  // boxes of the tile; cells of a box; this lane's coordinates
-};
-__device__ __forceinline__ TileBoxes tile_boxes(const PagedWalk& w, int lane) {
-  const PagedAttentionParams& p = *w.p;
-  TileBoxes t;
-  t.rows = min(1 << p.m.page_shift, BN);
-  t.n = (min(BN, w.kend - w.j * BN) + t.rows - 1) / t.rows;
-  t.c1 = t.c2 = 0;
-  if (lane < t.n) {
-    const int cell = w.j * BN + lane * t.rows;
-    const int pid = paged_page(p.m, w.a, cell);
-    if (pid < 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
-    t.c1 = cell & ((1 << p.m.page_shift) - 1);
-    t.c2 = pid < 0 ? -1 : pid * p.H_kv + w.g;  // outside the map: zeros
+  int rows, n;    // cells of a box; boxes of the tile
+  int entry;      // this lane's table entry, of tile j
+  int j;
+  __device__ __forceinline__ void fetch(const PagedWalk& w, int lane, int tile) {
+    j = tile;
+    const int cell = tile * BN + lane * rows;
+    entry = 0;
+    if (lane < BN / rows && cell < w.kend) entry = paged_entry(w.p->m, w.a, cell);
   }
-  return t;
-}
+  // Of a segment's first tile.
+  __device__ __forceinline__ void start(const PagedWalk& w, int lane) {
+    rows = min(1 << w.p->m.page_shift, BN);
+    fetch(w, lane, w.j);
+  }
+  // This lane's group of rows in the pool.
+  __device__ __forceinline__ int group(const PagedWalk& w, int lane) {
+    n = (min(BN, w.kend - w.j * BN) + rows - 1) / rows;
+    if (lane < n && (entry < 0 || entry >= w.p->m.P)) atomicOr(w.p->status, KVGQA_FLAG_PAGE_RANGE);
+    return paged_tile_group(w.p->m, entry, w.p->H_kv, w.g, w.j * BN + lane * rows);
+  }
+};
 
 // Atomic add with release and acquire semantics at GPU scope.
 __device__ __forceinline__ int atomic_add_acq_rel_gpu(int* ptr, int v) {
@@ -444,6 +451,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       return true;
     };
     bool turns = false;  // the last tile went to one group
+    TileBoxes t;
     for (; walk.ok; walk.advance()) {
       const bool fresh = walk.fresh(), dual = walk.dual();
       if (dual && turns) {
@@ -456,17 +464,17 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         if (!dry) break;
       }
       turns = !dual;
+      if (fresh) t.start(walk, lane);
       if (fresh && !load_q(dual ? 0 : walk.slot, 0)) break;
       const int s = it % C::NK;
-      const TileBoxes t = tile_boxes(walk, lane);
       if (it >= C::NK && !KVGQA_WAIT(&k_empty[s], ((it / C::NK) - 1) & 1)) break;
+      const int group = t.group(walk, lane);
       if (lane == 0) mbar_arrive_expect_tx(&k_full[s], t.n * t.rows * 128 * C::NSUB);
       __syncwarp();
-      if (lane < t.n) {
-        unsigned char* st = smem + C::K_OFF + s * C::TILE + lane * t.rows * 128;
-        for (int sub = 0; sub < C::NSUB; ++sub)
-          tma_load_3d(st + sub * SUB, &map_k, sub * 64, t.c1, t.c2, &k_full[s], pol_kv);
-      }
+      if (lane < t.n)
+        tma_load_4d(smem + C::K_OFF + s * C::TILE + lane * t.rows * 128 * C::NSUB, &map_k, 0, 0, 0, group, &k_full[s],
+                    pol_kv);
+      t.fetch(walk, lane, walk.j + 1);
       ++it;
       if (fresh && dual && !load_q(1, 1)) break;
     }
@@ -482,18 +490,19 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     // ------------------------------------------------------------ V producer
     const uint64_t pol_kv = l2_evict_last_policy();
     int it = 0, landed = 0;
+    TileBoxes t;
     for (; walk.ok; walk.advance()) {
       const int s = it % C::NV;
-      const TileBoxes t = tile_boxes(walk, lane);
+      if (walk.fresh()) t.start(walk, lane);
       if (it >= C::NV && !KVGQA_WAIT(&v_empty[s], ((it / C::NV) - 1) & 1)) break;
+      const int group = t.group(walk, lane);
       const int live = walk.kend - walk.j * BN;  // cells of this tile
       uint64_t* bar = live < BN ? v_land : &v_full[s];
       unsigned char* st = smem + C::V_OFF + s * C::TILE;
       if (lane == 0) mbar_arrive_expect_tx(bar, t.n * t.rows * 128 * C::NSUB);
       __syncwarp();
-      if (lane < t.n)
-        for (int sub = 0; sub < C::NSUB; ++sub)
-          tma_load_3d(st + sub * SUB + lane * t.rows * 128, &map_v, sub * 64, t.c1, t.c2, bar, pol_kv);
+      if (lane < t.n) tma_load_4d(st + lane * t.rows * 128 * C::NSUB, &map_v, 0, 0, 0, group, bar, pol_kv);
+      t.fetch(walk, lane, walk.j + 1);
       ++it;
       if (live < BN) {
         // the cells behind the last one weigh zero, and must not be NaN
@@ -502,7 +511,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         for (int i = live * 8 + lane; i < BN * 8; i += 32)
 #pragma unroll
           for (int sub = 0; sub < C::NSUB; ++sub)
-            *reinterpret_cast<uint4*>(st + sub * SUB + i * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(st + (i >> 6) * C::Tile::GROUP + sub * 1024 + (i & 63) * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_full[s]);
@@ -535,10 +544,10 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     bool prev_first = false, prev_alone = false;
     // O_x (+)= P_x V of tile `prev`, by the elected lane
     auto issue_pv = [&]() {
-      const uint32_t v_lo = smem_desc_lo(sbase + C::V_OFF + prev % C::NV * C::TILE, SUB);
+      const uint32_t v_lo = smem_desc_lo(sbase + C::V_OFF + prev % C::NV * C::TILE, 1024);
 #pragma unroll
       for (int ks = 0; ks < BN / 16; ++ks)
-        umma_f16_ts_lo(o_tm, s_tm + ks * 8, v_lo + ks * 128, IDESC_PV, (ks > 0 || !prev_first) ? 1u : 0u);
+        umma_f16_ts_lo<C::Tile::GROUP>(o_tm, s_tm + ks * 8, v_lo + ks * (2 * C::Tile::GROUP >> 4), IDESC_PV, (ks > 0 || !prev_first) ? 1u : 0u);
     };
     auto release_v = [&]() {
       uint64_t* free = &v_empty[prev % C::NV];
@@ -599,7 +608,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t o = (ks % 4) * (32 >> 4);
-            umma_f16_ss_lo(s_tm, q_lo + (ks / 4) * (C::QSUB >> 4) + o, k_lo + (ks / 4) * (SUB >> 4) + o, IDESC_QK, ks > 0);
+            umma_f16_ss_lo<1024, C::Tile::GROUP>(s_tm, q_lo + (ks / 4) * (C::QSUB >> 4) + o,
+                                                 k_lo + (ks / 4) * (1024 >> 4) + o, IDESC_QK, ks > 0);
           }
           umma_commit(&s_full[x]);
           umma_commit(&k_empty[kn]);
@@ -984,16 +994,9 @@ cudaError_t make_maps(const PagedAttentionParams& p, Maps* m) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  const cuuint64_t page = 1ull << p.m.page_shift;
-  for (int t = 0; t < 2; ++t) {
-    const cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(p.m.P) * Hkv};
-    const cuuint64_t strides[2] = {D * 2, D * 2 * page};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page < BN ? page : BN), 1};
-    if (enc(t == 0 ? &m->k : &m->v, type, 3, const_cast<uint16_t*>(t == 0 ? p.k_cache : p.v_cache), dims, strides, box,
-            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
+  if (paged_tile_map(enc, &m->k, type, p.k_cache, p.D, p.m.P, p.H_kv, p.m.page_shift) != CUDA_SUCCESS ||
+      paged_tile_map(enc, &m->v, type, p.v_cache, p.D, p.m.P, p.H_kv, p.m.page_shift) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   return cudaSuccess;
 }
 

@@ -37,6 +37,7 @@
 
 #include "elem.cuh"
 #include "paged.cuh"
+#include "paged_tiles.cuh"
 #include "tcgen05.cuh"
 
 namespace kvgqa {
@@ -46,7 +47,7 @@ constexpr int BK = 128;        // cells of a tile (= MMA M = TMEM lanes)
 constexpr int ITEM = 2 * BK;   // cells of an item
 constexpr int BC = 128;        // columns of a block
 constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
-constexpr int THREADS = 11 * 32;
+constexpr int THREADS = 12 * 32;
 constexpr int W_K = 8, W_Q = 9, W_MMA = 10;
 constexpr int TMEM_COLS = 512; // S^T of A and B, two buffers each, 128 columns
 constexpr int kQueryBlocks = 2; // query blocks in flight, or resident
@@ -56,7 +57,8 @@ constexpr unsigned FULLMASK = 0xffffffffu;
 template <int D>
 struct MCfg {
   static constexpr int NSUB = D / 64;
-  static constexpr int TILE = NSUB * SUB;
+  using Tile = PagedTile<D>;
+  static constexpr int TILE = Tile::BYTES;          // of cells, or a query block
   static constexpr int NK = D == 128 ? 2 : 4;       // items in flight
   static constexpr int NQ = kQueryBlocks;
   static constexpr int K_OFF = 0;
@@ -66,7 +68,7 @@ struct MCfg {
   // k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NL], l_empty[NL], s_full[4], s_empty[4], drain
   static constexpr int SEQ_OFF = SCR_OFF + 64 * 4;  // the walk's sequences
   static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * sizeof(PagedSeq);
-  static constexpr int NBAR = 2 * NK + 2 * NQ + 2 * NL + 9;
+  static constexpr int NBAR = 2 * NK + 2 * NQ + 2 * NL + 10;
   static constexpr int SLOT_OFF = BAR_OFF + NBAR * 8;
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
   static constexpr int SMEM = FLAG_OFF + 16 + 1024;
@@ -166,6 +168,50 @@ struct MassWalk {
   }
 };
 
+// Adds the weights of a block's columns to a cell's sum: exp2 of the scaled
+// scores less the columns' log sums, 32 columns at a time, the next read while
+// the weights of one lot are computed.  PICKED: only columns lo .. hi - 1 count
+// (a block at a sequence's end, or over cells that some of its tokens do not
+// see; what is in the others may be anything).
+__device__ __forceinline__ uint32_t span_mask(int lo, int hi) {  // bits lo .. hi - 1 of 32
+  const uint32_t below = hi >= 32 ? 0xffffffffu : (1u << max(hi, 0)) - 1u;
+  return lo >= 32 ? 0u : below >> max(lo, 0) << max(lo, 0);
+}
+template <bool PICKED>
+__device__ __forceinline__ void add_lot(const uint32_t (&u)[32], const float* ls, float2 c2, uint32_t m, float2& s0, float2& s1) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
+    float2 xa = ffma2(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), c2, make_float2(l4.x, l4.y));
+    float2 xb = ffma2(make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), c2, make_float2(l4.z, l4.w));
+    if (PICKED) {
+      xa.x = m >> i & 1 ? xa.x : -INFINITY;
+      xa.y = m >> (i + 1) & 1 ? xa.y : -INFINITY;
+      xb.x = m >> (i + 2) & 1 ? xb.x : -INFINITY;
+      xb.y = m >> (i + 3) & 1 ? xb.y : -INFINITY;
+    }
+    s0 = fadd2(s0, make_float2(ex2(xa.x), ex2(xa.y)));
+    s1 = fadd2(s1, make_float2(ex2(xb.x), ex2(xb.y)));
+  }
+}
+template <bool PICKED>
+__device__ __forceinline__ void add_columns(uint32_t s_tm, const float* ls, float2 c2, int lo, int hi, float2& sum) {
+  uint32_t u0[32], u1[32];
+  float2 sum1 = make_float2(0.f, 0.f);
+  tmem_ld32(s_tm, u0);
+#pragma unroll 1
+  for (int q = 0; q < (PICKED ? hi : BC); q += 64) {
+    tmem_wait_ld();
+    tmem_ld32(s_tm + q + 32, u1);
+    add_lot<PICKED>(u0, ls + q, c2, PICKED ? span_mask(lo - q, hi - q) : 0, sum, sum1);
+    tmem_wait_ld();
+    if (q + 64 < BC) tmem_ld32(s_tm + q + 64, u0);
+    add_lot<PICKED>(u1, ls + q + 32, c2, PICKED ? span_mask(lo - q - 32, hi - q - 32) : 0, sum, sum1);
+  }
+  tmem_wait_ld();
+  sum = fadd2(sum, sum1);
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(THREADS, 1)
 paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_constant__ CUtensorMap map_q,
@@ -197,11 +243,11 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);  // both issuers
     }
     for (int s = 0; s < C::NQ; ++s) {
       mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
+      mbar_init(&q_empty[s], 2);
     }
     for (int s = 0; s < NL; ++s) {
       mbar_init(&l_full[s], 1);
@@ -211,7 +257,8 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
       mbar_init(&s_full[s], 1);
       mbar_init(&s_empty[s], 4);  // one arrival per warp of the tile's group
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -244,28 +291,25 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     // ------------------------------------------------------------ K producer
     const uint64_t pol = l2_evict_first_policy();  // each cell is read once
     const int rows = min(1 << p.m.page_shift, BK);
-    int it = 0;
-    for (; walk.ok; walk.advance(), ++it) {
+    // box i of an item holds the cells kb * ITEM + i * rows ..; at most 16.  A
+    // lane's table entry is read an item ahead within a head.
+    auto fetch = [&](int kb) {
+      const int cell = kb * ITEM + lane * rows;
+      return lane < ITEM / rows && cell < walk.kl ? paged_entry(p.m, walk.a, cell) : 0;
+    };
+    int it = 0, entry = fetch(walk.kb);
+    for (; walk.ok; ++it) {
       const int s = it % C::NK;
-      // box i of the item holds the cells kb * ITEM + i * rows ..; at most 16
       const int n = (min(ITEM, walk.kl - walk.kb * ITEM) + rows - 1) / rows;
-      int c1 = 0, c2 = 0;
-      if (lane < n) {
-        const int cell = walk.kb * ITEM + lane * rows;
-        const int pid = paged_page(p.m, walk.a, cell);
-        if (pid < 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
-        c1 = cell & ((1 << p.m.page_shift) - 1);
-        c2 = pid < 0 ? -1 : pid * p.H_kv + walk.g;  // outside the map: zeros
-      }
       if (it >= C::NK && !KVGQA_WAIT(&k_empty[s], ((it / C::NK) - 1) & 1)) break;
+      if (lane < n && (entry < 0 || entry >= p.m.P)) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
+      const int group = paged_tile_group(p.m, entry, p.H_kv, walk.g, walk.kb * ITEM + lane * rows);
       if (lane == 0) mbar_arrive_expect_tx(&k_full[s], n * rows * 128 * C::NSUB);
       __syncwarp();
-      if (lane < n) {
-        const int r = lane * rows;
-        unsigned char* st = smem + C::K_OFF + (s * 2 + r / BK) * C::TILE + r % BK * 128;
-        for (int sub = 0; sub < C::NSUB; ++sub)
-          tma_load_3d(st + sub * SUB, &map_k, sub * 64, c1, c2, &k_full[s], pol);
-      }
+      if (lane < n)
+        tma_load_4d(smem + C::K_OFF + s * 2 * C::TILE + lane * rows * 128 * C::NSUB, &map_k, 0, 0, 0, group, &k_full[s], pol);
+      walk.advance();
+      if (walk.ok) entry = fetch(walk.kb);
     }
     __syncwarp();
     if (*abort_flag) {
@@ -319,50 +363,49 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
       for (int t = n - C::NQ < 0 ? 0 : n - C::NQ; t < n; ++t)
         mbar_wait_bounded(&q_full[t % C::NQ], (t / C::NQ) & 1, &none, nullptr);
     }
-  } else if (warp == W_MMA) {
-    // ------------------------------------------------------------ MMA issuer
-    int it = 0, sn[2] = {0, 0};
+  } else if (warp >= W_MMA) {
+    // ------------------------------------------------------------ MMA issuers, one per tile
+    const int x = uniform(warp - W_MMA);
+    int it = 0, sn = 0;
     bool ok = true, issued = false;
     for (; walk.ok && ok; walk.advance(), ++it) {
       const int ks = it % C::NK;
       const bool resident = walk.resident();
       if (!KVGQA_WAIT(&k_full[ks], (it / C::NK) & 1)) break;
-      const int fb0 = walk.first_block(0), fb1 = walk.first_block(1), tiles = walk.tiles();
+      const int fb0 = walk.first_block(0), fb = walk.live(x) > 0 ? walk.first_block(x) : walk.nblk;
       if (resident && walk.fresh)
         for (int n = walk.loads; n < walk.loads + walk.nblk && ok; ++n) ok = KVGQA_WAIT(&q_full[n % C::NQ], (n / C::NQ) & 1);
       if (!ok) break;
+      const uint32_t k_lo = smem_desc_lo(uniform(sbase + C::K_OFF + (ks * 2 + x) * C::TILE), 16);
       for (int blk = fb0; blk < walk.nblk; ++blk) {
         const int n = walk.loads + (resident ? blk : blk - fb0), qs = n % C::NQ;
         if (!resident) ok = KVGQA_WAIT(&q_full[qs], (n / C::NQ) & 1);
         if (!ok) break;
-        // only the columns that hold a query, in whole groups of 16
-        const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
-        const uint32_t idesc = uniform(idesc_f16kind_f32(E::kMmaFormat, BK, (cols + 15) & ~15, 0));
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (x == 1 && (tiles < 2 || blk < fb1)) continue;
-          const int buf = x * 2 + (sn[x] & 1);
-          if (sn[x] >= 2) {
-            ok = KVGQA_WAIT(&s_empty[buf], ((sn[x] >> 1) - 1) & 1);
-            if (!ok) break;
-          }
-          ++sn[x];
-          tc_fence_after();
-          const uint32_t k_lo = smem_desc_lo(sbase + C::K_OFF + (ks * 2 + x) * C::TILE, 16);
+        if (blk >= fb) {
+          const int buf = x * 2 + (sn & 1);
+          // only the columns that hold a query, in whole groups of 16
+          const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
+          const uint32_t idesc = uniform(idesc_f16kind_f32(E::kMmaFormat, BK, (cols + 15) & ~15, 0));
           const uint32_t q_lo = smem_desc_lo(uniform(sbase + C::Q_OFF + qs * C::TILE), 16);
           const uint32_t s_tm = uniform(tmem + buf * BC);
+          if (sn >= 2) {
+            ok = KVGQA_WAIT(&s_empty[buf], ((sn >> 1) - 1) & 1);
+            if (!ok) break;
+          }
+          ++sn;
+          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t o = (kk / 4) * (SUB >> 4) + (kk % 4) * (32 >> 4);
-              umma_f16_ss_lo(s_tm, k_lo + o, q_lo + o, idesc, kk > 0);
+              const uint32_t o = (kk % 4) * (32 >> 4);
+              umma_f16_ss_lo<C::Tile::GROUP, 1024>(s_tm, k_lo + (kk / 4) * (1024 >> 4) + o, q_lo + (kk / 4) * (SUB >> 4) + o,
+                                                     idesc, kk > 0);
             }
             umma_commit(&s_full[buf]);
           }
           __syncwarp();
           issued = true;
         }
-        if (!ok) break;
         if (!resident) {
           if (elect_one()) umma_commit(&q_empty[qs]);
           __syncwarp();
@@ -377,10 +420,10 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
       __syncwarp();
     }
     if (*abort_flag && issued) {
-      if (elect_one()) umma_commit(drain);
+      if (elect_one()) umma_commit(&drain[x]);
       __syncwarp();
       volatile int none = 0;
-      mbar_wait_bounded(drain, 0, &none, nullptr);
+      mbar_wait_bounded(&drain[x], 0, &none, nullptr);
     }
   } else {
     // ------------------------------------------------------------ weights (warps 0-7)
@@ -427,12 +470,7 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
           const float* ls = lse_s + (n % NL) * BC;
           const int cols = min(BC, (walk.ql << p.gp_shift) - blk * BC);
           const uint32_t s_tm = tmem + lane_base + buf * BC;
-          // 32 columns at a time, the next read while the weights of one lot are
-          // computed.  In a block at a sequence's end, or over cells that some of
-          // its tokens do not see, columns are picked one by one.
-          const bool picked = blk * BC < c_tile;
           const int lo = c_min - blk * BC;
-          float2 sum1 = make_float2(0.f, 0.f);
           if (cols <= 16) {  // single tokens: their heads alone
             uint32_t u[16];
             tmem_ld16(s_tm, u);
@@ -442,39 +480,14 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
               const float w = ex2(fmaf(__uint_as_float(u[i]), p.scale_log2, ls[i]));
               sum.x += i >= lo && i < cols ? w : 0.f;
             }
+          } else if (cols == BC && blk * BC >= c_tile) {
+            add_columns<false>(s_tm, ls, c2, 0, BC, sum);
           } else {
-            uint32_t u[2][32];
-            tmem_ld32(s_tm, u[0]);
-#pragma unroll
-            for (int q = 0; q < BC; q += 32) {
-              if (q < cols) {  // uniform
-                tmem_wait_ld();
-                if (q + 32 < BC) tmem_ld32(s_tm + q + 32, u[(q / 32 + 1) & 1]);
-                const float* sv = reinterpret_cast<const float*>(u[(q / 32) & 1]);
-                if (!picked && q + 32 <= cols) {
-#pragma unroll
-                  for (int i = 0; i < 32; i += 4) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(ls + q + i);
-                    const float2 xa = ffma2(make_float2(sv[i], sv[i + 1]), c2, make_float2(l4.x, l4.y));
-                    const float2 xb = ffma2(make_float2(sv[i + 2], sv[i + 3]), c2, make_float2(l4.z, l4.w));
-                    sum = fadd2(sum, make_float2(ex2(xa.x), ex2(xa.y)));
-                    sum1 = fadd2(sum1, make_float2(ex2(xb.x), ex2(xb.y)));
-                  }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const float w = ex2(fmaf(sv[i], p.scale_log2, ls[q + i]));
-                    sum.x += q + i >= lo && q + i < cols ? w : 0.f;
-                  }
-                }
-              }
-            }
+            add_columns<true>(s_tm, ls, c2, lo, cols, sum);
           }
-          tmem_wait_ld();  // (the read ahead of a short block's last lot)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_empty[buf]);
-          sum = fadd2(sum, sum1);
           if (!resident) pass(n);
         }
         if (!ok) break;
@@ -535,7 +548,7 @@ cudaError_t launch_paged_mass(const PagedMassParams& params, cudaStream_t stream
   auto enc = tma_encoder();
   if (!enc) return cudaErrorNotSupported;
   const CUtensorMapDataType type = p.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const cuuint64_t D = p.D, G = p.G, Hkv = p.H_kv, page = 1ull << p.m.page_shift;
+  const cuuint64_t D = p.D, G = p.G, Hkv = p.H_kv;
   const cuuint32_t es[4] = {1, 1, 1, 1};
   CUtensorMap mq, mk;
   {
@@ -547,15 +560,8 @@ cudaError_t launch_paged_mass(const PagedMassParams& params, cudaStream_t stream
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  {
-    const cuuint64_t dims[3] = {D, page, static_cast<cuuint64_t>(p.m.P) * Hkv};
-    const cuuint64_t strides[2] = {D * 2, D * 2 * page};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page < BK ? page : BK), 1};
-    if (enc(&mk, type, 3, const_cast<uint16_t*>(p.k_cache), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
+  if (paged_tile_map(enc, &mk, type, p.k_cache, p.D, p.m.P, p.H_kv, p.m.page_shift) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   if (p.D == 128) return p.f16 ? launch_d<128, true>(p, mq, mk, stream) : launch_d<128, false>(p, mq, mk, stream);
   if (p.D == 64) return p.f16 ? launch_d<64, true>(p, mq, mk, stream) : launch_d<64, false>(p, mq, mk, stream);
   return cudaErrorInvalidValue;

@@ -95,24 +95,28 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t smem_addr, uint32_t
 }
 
 // The same matrix descriptor as its low word, whose value moves with the
-// address (16-byte units), and a high word that is the same for every operand
-// with 1024 bytes between groups of 8 rows: adding to the low word steps through a
-// tile, which costs the issuing thread one addition per operand.
-constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+// address (16-byte units), and a high word that depends on the bytes between
+// groups of 8 rows alone: adding to the low word steps through a tile, which
+// costs the issuing thread one addition per operand.
+__host__ __device__ constexpr uint32_t desc_hi_sw128(uint32_t group_bytes) {
+  return (group_bytes >> 4) | (1u << 14) | (2u << 29);
+}
 __device__ __forceinline__ uint32_t smem_desc_lo(uint32_t smem_addr, uint32_t lbo_bytes) {
   return ((smem_addr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
 }
+template <uint32_t A_GROUP = 1024, uint32_t B_GROUP = 1024>
 __device__ __forceinline__ void umma_f16_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %5};\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(desc_hi_sw128(A_GROUP)), "n"(desc_hi_sw128(B_GROUP))
       : "memory");
 }
+template <uint32_t B_GROUP = 1024>
 __device__ __forceinline__ void umma_f16_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -120,7 +124,7 @@ __device__ __forceinline__ void umma_f16_ts_lo(uint32_t d_tmem, uint32_t a_tmem,
       "mov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHiSw128)
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(desc_hi_sw128(B_GROUP))
       : "memory");
 }
 
