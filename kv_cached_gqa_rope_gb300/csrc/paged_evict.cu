@@ -9,8 +9,9 @@
 // mass by a radix select over order-preserving 32-bit keys, 11 + 11 + 10 bits
 // a pass with a histogram in shared memory, then the list of kept cells in
 // ascending order by counting: each warp owns a contiguous stripe, counts its
-// kept cells by ballots, and writes them from its prefix on.  The masses are
-// read five times, from L2 after the first.
+// kept cells by ballots, and writes them from its prefix on.  The masses of up to
+// kCachedCells cells are read once and kept in shared memory; those of longer
+// sequences are read five times, from L2 after the first.
 //
 // Kernel 2 moves K and V in place: one read and one write of each kept cell
 // that moves.  A kept cell's new place is never behind its old one, so in
@@ -33,7 +34,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kCachedCells = 9216;  // 36 KB of keys beside the histogram: no more than a CTA may have by default
+constexpr int kCachedCells = 9216;  // 36 KB of masses beside the histogram: no more than a CTA may have by default
 
 // Keys in the order of the masses: NaN lowest, then -inf .. +inf, both zeros alike.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -42,17 +43,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Whether every page of the sequence's n cells is a page of the pool (asked by
-// the whole CTA).
-__device__ __forceinline__ bool pages_ok(const PagedMeta& m, int a, int n) {
-  bool ok = true;
-  for (int c = threadIdx.x << m.page_shift; c < n; c += blockDim.x << m.page_shift) ok = ok && paged_page(m, a, c) >= 0;
-  return __syncthreads_and(ok);
-}
-
 template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
-  extern __shared__ uint32_t keys[];  // CACHED: the keys of all cells
+  extern __shared__ float cells[];  // CACHED: the masses of all cells
   __shared__ int hist[kBins];
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ uint32_t sel_digit;
@@ -61,19 +54,39 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  const int n = p.m.kv_lengths[a];
-  if (n < 0 || n > p.m.max_cells) {
-    if (g == 0 && tid == 0) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
-    return;
-  }
-  if (n > p.keep && !pages_ok(p.m, a, n)) {
-    if (g == 0 && tid == 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
-    return;
-  }
   const size_t head = static_cast<size_t>(a) * p.H_kv + g;
   const float* mass = p.mass + head * p.mass_cells;
   float* mass_out = p.mass_out + head * p.mass_cells;
   int32_t* kept = p.kept + head * p.keep;
+  const int n = p.m.kv_lengths[a];
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
+  if (n < 0 || n > p.m.max_cells) {
+    if (g == 0 && tid == 0) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
+    return;
+  }
+  const int old = n - p.recent;
+  if (n > p.keep) {
+    // The masses are read once, and the first digits counted, while the table's
+    // entries are on their way.
+    const int page = tid << p.m.page_shift;
+    const int entry = page < n ? paged_page(p.m, a, page) : 0;
+    if constexpr (CACHED) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kSelThreads) {
+        const float x = mass[i];
+        cells[i] = x;
+        if (i < old) atomicAdd(&hist[order_key(x) >> 21], 1);
+      }
+    }
+    bool ok = entry >= 0;
+    for (int c = page + (kSelThreads << p.m.page_shift); c < n; c += kSelThreads << p.m.page_shift)
+      ok = ok && paged_page(p.m, a, c) >= 0;
+    if (!__syncthreads_and(ok)) {
+      if (g == 0 && tid == 0) atomicOr(p.status, KVGQA_FLAG_PAGE_RANGE);
+      return;
+    }
+  }
   const int m = min(n, p.keep);
   if (g == 0 && tid == 0) p.new_lengths[a] = m;
   for (int i = m + tid; i < p.mass_cells; i += kSelThreads) mass_out[i] = 0.f;
@@ -86,19 +99,14 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
     return;
   }
 
-  if constexpr (CACHED) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kSelThreads) keys[i] = order_key(mass[i]);
-    __syncthreads();
-  }
-  auto key_of = [&](int i) {
-    if constexpr (CACHED) return keys[i];
-    else return order_key(mass[i]);
+  auto mass_of = [&](int i) {
+    if constexpr (CACHED) return cells[i];
+    else return mass[i];
   };
+  auto key_of = [&](int i) { return order_key(mass_of(i)); };
 
   // The smallest key that is kept among the old cells, and how many cells of
   // that very key are.
-  const int old = n - p.recent;
   uint32_t thr = 0;       // digits found so far
   int need = p.keep - p.recent;
   if (need > 0) {
@@ -108,19 +116,22 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
       const int bits = pass == 2 ? 10 : 11;
       const uint32_t above = shift == 32 ? 0u : ~0u << shift;  // digits already fixed
       shift -= bits;
-      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
+      if (!CACHED || pass > 0) {
 #pragma unroll 4
-      for (int i = tid; i < old; i += kSelThreads) {
-        const uint32_t k = key_of(i);
-        if ((k & above) == thr) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+        for (int i = tid; i < old; i += kSelThreads) {
+          const uint32_t k = key_of(i);
+          if ((k & above) == thr) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+        }
+        __syncthreads();
       }
-      __syncthreads();
       // From the highest digit down: the first at which the count reaches need.
       // Thread t holds the 4 digits below kBins - 4t.
       int c[4], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum += c[i] = hist[kBins - 1 - 4 * tid - i];
+      for (int i = 0; i < 4; ++i) {
+        sum += c[i] = hist[kBins - 1 - 4 * tid - i];
+        hist[kBins - 1 - 4 * tid - i] = 0;  // for the next digits
+      }
       int incl = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
     if (take) {
       const int to = at + __popc(tm & below);
       kept[to] = i;
-      mass_out[to] = mass[i];
+      mass_out[to] = mass_of(i);
     }
     at += __popc(tm);
     eq_before += __popc(eqm);
@@ -283,7 +294,7 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // The keys are kept in shared memory up to kCachedCells cells a row; longer rows are read from L2 in each pass.
+  // The masses are kept in shared memory up to kCachedCells cells a row; longer rows are read from L2 in each pass.
   const bool cached = p.mass_cells <= kCachedCells;
   cfg.dynamicSmemBytes = cached ? static_cast<size_t>(p.mass_cells) * sizeof(uint32_t) : 0;
   const cudaError_t e = cached ? cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<true>, p)
