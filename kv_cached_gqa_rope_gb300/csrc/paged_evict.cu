@@ -31,8 +31,9 @@ namespace kvgqa {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+static_assert(kSelWarps <= 32, "a warp adds up the warps' counts");
 constexpr int kBins = 2048;
 constexpr int kCachedCells = 9216;  // 36 KB of masses beside the histogram: no more than a CTA may have by default
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 
 template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
   extern __shared__ float cells[];  // CACHED: the masses of all cells
   __shared__ int hist[kBins];
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
@@ -125,12 +126,13 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
         __syncthreads();
       }
       // From the highest digit down: the first at which the count reaches need.
-      // Thread t holds the 4 digits below kBins - 4t.
-      int c[4], sum = 0;
+      // Thread t holds the kShare digits below kBins - kShare t.
+      constexpr int kShare = kBins / kSelThreads;
+      int c[kShare], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum += c[i] = hist[kBins - 1 - 4 * tid - i];
-        hist[kBins - 1 - 4 * tid - i] = 0;  // for the next digits
+      for (int i = 0; i < kShare; ++i) {
+        sum += c[i] = hist[kBins - 1 - kShare * tid - i];
+        hist[kBins - 1 - kShare * tid - i] = 0;  // for the next digits
       }
       int incl = sum;
 #pragma unroll
@@ -140,12 +142,11 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
       }
       if (lane == 31) warp_gt[warp] = incl;
       __syncthreads();
-      int before = incl - sum;
-      for (int w = 0; w < warp; ++w) before += warp_gt[w];
+      int before = incl - sum + __reduce_add_sync(FULL, lane < warp ? warp_gt[lane] : 0);
       if (before < need && before + sum >= need) {
         int i = 0;
         while (before + c[i] < need) before += c[i++];
-        sel_digit = kBins - 1 - 4 * tid - i;
+        sel_digit = kBins - 1 - kShare * tid - i;
         sel_need = need - before;
       }
       __syncthreads();
@@ -178,12 +179,9 @@ __global__ void __launch_bounds__(kSelThreads) paged_evict_select_kernel(const _
     warp_eq[warp] = eqs;
   }
   __syncthreads();
-  int eq_before = 0, at = 0;  // cells of the threshold's key before this stripe; kept cells before it
-  for (int w = 0; w < warp; ++w) {
-    at += warp_gt[w];
-    eq_before += warp_eq[w];
-  }
-  at += min(eq_before, need);
+  // cells of the threshold's key before this stripe; kept cells before it
+  int eq_before = __reduce_add_sync(FULL, lane < warp ? warp_eq[lane] : 0);
+  int at = __reduce_add_sync(FULL, lane < warp ? warp_gt[lane] : 0) + min(eq_before, need);
   for (int i = s0 + lane; i < s0 + S; i += 32) {
     bool gt, eq;
     classify(i, gt, eq);
