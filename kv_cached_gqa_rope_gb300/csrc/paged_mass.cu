@@ -14,18 +14,28 @@
 // An item is 256 cells of one sequence and KV head (two 128-cell tiles, A and
 // B).  The queries of the KV group are its columns, (token, head of the group)
 // with the group padded to a power of two, in blocks of 128.  Per item:
-//   warp 8      TMA of the two K tiles, one box per page (2-stage ring);
-//   warp 9      TMA of the query blocks (ring) and their log sums, as base-2
-//               logs, into shared memory (+inf for columns without a query); a
+//   warp 8      TMA of the two K tiles, one box per page (ring of 2 items, 4 at D = 64);
+//   warp 9      TMA of the query blocks (ring) and their log sums, as negated
+//               base-2 logs, into shared memory (-inf for columns without a query); a
 //               head's blocks stay there for all of its items if they fit the ring;
-//   warp 10     S_x^T = K_x Q^T of each block into TMEM (x = A, B, two buffers each);
+//   warps 10, 11 S_x^T = K_x Q^T of each block into TMEM (x = A, B, two buffers each);
 //   warps 0-3   tile A, warps 4-7 tile B: exp2 of the scaled scores less the
 //               column's log sum, added to the cell's sum; at the item's end
 //               each thread adds that to its cell (as a reduction in L2: a
 //               load would have to be waited for).
 // The items are dealt as contiguous equal shares of their column blocks to a
-// persistent grid.  Single tokens are bound by the stream of K, longer chunks
-// by the exponentials.
+// persistent grid.
+//
+// What bounds it, as measured (32 query heads, 8 KV heads of 128): single tokens by
+// the stream of K and about 5 us of start and end (32 sequences of up to 4095 cells,
+// pages of 16: 25.6 us, 5.4 TB/s of cells; with a copy per page and half of a head
+// the producer warp was the bound, 27.8 us).  Windows of 64 tokens over 4000-16000
+// cells take 50 us (0.79 PFLOP/s, 3.3 TB/s) where the MMAs, the exponentials and the
+// stream would each take 17-24: a block of 128 columns costs a softmax warp 1700
+// clocks, of which the special-function unit is busy 1024 with both tiles' warps,
+// and an item about 1500 of waits and set-up beside its blocks.  Two warps more a
+// tile, with their sums joined through shared memory, measured 48 us on windows
+// but 28.5 on single tokens; 128 columns in registers at once spill (69).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,9 +56,9 @@ namespace {
 constexpr int BK = 128;        // cells of a tile (= MMA M = TMEM lanes)
 constexpr int ITEM = 2 * BK;   // cells of an item
 constexpr int BC = 128;        // columns of a block
-constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile
+constexpr int SUB = 16384;     // one [128 rows x 64 16-bit values] swizzled sub-tile of a query block
 constexpr int THREADS = 12 * 32;
-constexpr int W_K = 8, W_Q = 9, W_MMA = 10;
+constexpr int W_K = 8, W_Q = 9, W_MMA = 10;  // and W_MMA + 1
 constexpr int TMEM_COLS = 512; // S^T of A and B, two buffers each, 128 columns
 constexpr int kQueryBlocks = 2; // query blocks in flight, or resident
 constexpr int NL = 8;          // log-sum slots
@@ -159,7 +169,6 @@ struct MassWalk {
   __device__ __forceinline__ bool last() const { return kb + 1 == n_items || v + units >= v1; }  // of this head, here
   // Cells of tile x of the item.
   __device__ __forceinline__ int live(int x) const { return min(BK, kl - kb * ITEM - x * BK); }
-  __device__ __forceinline__ int tiles() const { return live(1) > 0 ? 2 : 1; }
   // The first column block of which some token sees a cell of tile x (the
   // last token sees every cell, so the last block always counts).
   __device__ __forceinline__ int first_block(int x) const {
@@ -168,32 +177,39 @@ struct MassWalk {
   }
 };
 
-// Adds the weights of a block's columns to a cell's sum: exp2 of the scaled
-// scores less the columns' log sums, 32 columns at a time, the next read while
-// the weights of one lot are computed.  PICKED: only columns lo .. hi - 1 count
-// (a block at a sequence's end, or over cells that some of its tokens do not
-// see; what is in the others may be anything).
-__device__ __forceinline__ uint32_t span_mask(int lo, int hi) {  // bits lo .. hi - 1 of 32
+// Bits lo .. hi - 1 of 32.
+__device__ __forceinline__ uint32_t span_mask(int lo, int hi) {
   const uint32_t below = hi >= 32 ? 0xffffffffu : (1u << max(hi, 0)) - 1u;
   return lo >= 32 ? 0u : below >> max(lo, 0) << max(lo, 0);
 }
+
+// Adds the weights of 32 columns to two pairs of sums: exp2 of the scaled scores
+// less the columns' log sums.  PICKED: of the columns in the mask alone (what is
+// in the others may be anything).
 template <bool PICKED>
-__device__ __forceinline__ void add_lot(const uint32_t (&u)[32], const float* ls, float2 c2, uint32_t m, float2& s0, float2& s1) {
+__device__ __forceinline__ void add_lot(const uint32_t (&u)[32], const float* ls, float2 c2, uint32_t mask, float2& s0,
+                                        float2& s1) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
     float2 xa = ffma2(make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), c2, make_float2(l4.x, l4.y));
     float2 xb = ffma2(make_float2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), c2, make_float2(l4.z, l4.w));
     if (PICKED) {
-      xa.x = m >> i & 1 ? xa.x : -INFINITY;
-      xa.y = m >> (i + 1) & 1 ? xa.y : -INFINITY;
-      xb.x = m >> (i + 2) & 1 ? xb.x : -INFINITY;
-      xb.y = m >> (i + 3) & 1 ? xb.y : -INFINITY;
+      xa.x = mask >> i & 1 ? xa.x : -INFINITY;
+      xa.y = mask >> (i + 1) & 1 ? xa.y : -INFINITY;
+      xb.x = mask >> (i + 2) & 1 ? xb.x : -INFINITY;
+      xb.y = mask >> (i + 3) & 1 ? xb.y : -INFINITY;
     }
     s0 = fadd2(s0, make_float2(ex2(xa.x), ex2(xa.y)));
     s1 = fadd2(s1, make_float2(ex2(xb.x), ex2(xb.y)));
   }
 }
+
+// The same for a block's columns lo .. hi - 1 (not PICKED: all of them).  Two lots
+// in turn, one read from tensor memory while the other's weights are computed; in
+// a loop and without a choice inside it, since the whole block unrolled spills and
+// a branch per lot keeps the compiler from overlapping them (windows of 64 tokens:
+// 50 us; unrolled 52-64, with the choice inside 54).
 template <bool PICKED>
 __device__ __forceinline__ void add_columns(uint32_t s_tm, const float* ls, float2 c2, int lo, int hi, float2& sum) {
   uint32_t u0[32], u1[32];
@@ -208,7 +224,7 @@ __device__ __forceinline__ void add_columns(uint32_t s_tm, const float* ls, floa
     if (q + 64 < BC) tmem_ld32(s_tm + q + 64, u0);
     add_lot<PICKED>(u1, ls + q + 32, c2, PICKED ? span_mask(lo - q - 32, hi - q - 32) : 0, sum, sum1);
   }
-  tmem_wait_ld();
+  tmem_wait_ld();  // (the read ahead of a short block's last lot)
   sum = fadd2(sum, sum1);
 }
 
@@ -480,7 +496,7 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
               const float w = ex2(fmaf(__uint_as_float(u[i]), p.scale_log2, ls[i]));
               sum.x += i >= lo && i < cols ? w : 0.f;
             }
-          } else if (cols == BC && blk * BC >= c_tile) {
+          } else if (cols == BC && blk * BC >= c_tile) {  // every column, by every cell of the tile
             add_columns<false>(s_tm, ls, c2, 0, BC, sum);
           } else {
             add_columns<true>(s_tm, ls, c2, lo, cols, sum);
