@@ -834,6 +834,8 @@ PagedViews paged_meta(kvgqa::PagedMeta* m, const kvgqa_tensor* query_starts, boo
   const int shift = page_shift_of(page);
   if (N > (1ll << 30) || A > (1ll << 30)) fail(KVGQA_EUNSUPPORTED, "more than 2^30 tokens or sequences");
   if (!product_below({P, H_kv}, 1ll << 31)) fail(KVGQA_EUNSUPPORTED, "P*H_kv must stay below 2^31");
+  // (the kernels that read tiles count the pool's rows in groups of 8, in 32 bits)
+  if (!product_below({P, H_kv, page}, 1ll << 34)) fail(KVGQA_EUNSUPPORTED, "P*H_kv*page must stay below 2^34");
   if (!product_below({max_pages, page}, (1ll << 30) + 1)) fail(KVGQA_EUNSUPPORTED, "max_pages*page must not exceed 2^30");
   m->A = (int)A;
   m->N = (int)N;

@@ -107,6 +107,23 @@ def test_shared_refusals(fn, args):
     assert code_of(fn, **args(workspace=torch.zeros(64, dtype=I32))) == "EWORKSPACE"
 
 
+@pytest.mark.parametrize("fn,args", CALLS)
+def test_pools_past_the_kernels_indexes_are_refused(fn, args, monkeypatch):
+    # 2^26 pages of 2 heads and 256 cells: 2^32 groups of 8 rows (no such memory
+    # exists; the descriptors say so)
+    plain = kv.describe
+
+    def described(t):
+        d = plain(t)
+        if t.dim() == 4:
+            d.shape[0], d.shape[2], d.bytes = 1 << 26, 256, 1 << 62
+            d.strides[0], d.strides[1] = 2 * 256 * 64, 256 * 64
+        return d
+
+    monkeypatch.setattr(kv, "describe", described)
+    assert code_of(fn, **args()) == "EUNSUPPORTED"
+
+
 def test_store_refusals():
     fn = kv.paged_rope_kv_store_out_
     assert code_of(fn, **store_args(theta=0.0)) == "EINVAL"
