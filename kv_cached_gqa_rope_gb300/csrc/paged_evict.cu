@@ -221,15 +221,17 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
   const int shift = p.m.page_shift, page = 1 << shift;
   const int n = p.m.kv_lengths[a];  // (an input of the call, like the table: not written by kernel 1)
   bool ok = n > p.keep && n <= p.m.max_cells;
-  if (!ok) return;  // uniform
-  const int n_pages = (n + page - 1) >> shift;
+  const int n_pages = ok ? (n + page - 1) >> shift : 0;
   for (int i = threadIdx.x; i < n_pages; i += kMoveThreads) {
     const int pid = paged_page(p.m, a, i << shift);
     ok = ok && pid >= 0;
     if (i < kTablePages) pages[i] = pid;
   }
-  if (!__syncthreads_and(ok)) return;
+  ok = __syncthreads_and(ok);
+  // Whether there is anything to move or not: the wait of the kernel behind this
+  // one covers this grid alone, and kernel 1 only through the wait in here.
   pdl_wait();
+  if (!ok) return;  // uniform
   const int32_t* kept = p.kept + (static_cast<size_t>(a) * p.H_kv + g) * p.keep;
   const int chunks = p.D / 8 / slices;              // 16-byte chunks of a row's slice (a power of two)
   const int step = kMoveThreads / chunks;           // rows that the CTA covers at a time
