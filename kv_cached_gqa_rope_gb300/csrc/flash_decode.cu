@@ -396,7 +396,11 @@ flash_decode_splitk_kernel(const __grid_constant__ DecodeParams p, const __grid_
   const int v1 = min(v0 + W, v_tot);
   Cursor<C::TK> cur;
   if (v0 < v_tot) cur.init(prefix, nkeys, p.H_kv, p.A, v0, v1);
-  if (v0 >= v_tot || !cur.more()) return;  // uniform: nothing allocated yet
+  if (v0 >= v_tot || !cur.more()) {  // uniform: nothing allocated yet
+    // (a step whose rows are all out of range has no producer that waits)
+    if constexpr (EARLY) pdl_wait();
+    return;
+  }
 
   // The tensor-memory address reaches the warps that use it through a
   // named barrier the producer (warp 4) does not join: it needs no tensor

@@ -70,3 +70,12 @@ def test_every_path_waits(file, name):
     bad, waited = unwaited_returns(dict(kernels(source(file)))[name])
     assert not bad, f"{name} returns without waiting for the kernel before it: {bad}"
     assert waited, f"{name} does not wait for the kernel before it on every path"
+
+
+def test_the_decode_step_s_early_start_waits():
+    """Its attention waits in the producer warp, behind the tiles it loads early:
+    a CTA without work has none, and waits before it returns."""
+    body = dict(kernels(source("flash_decode.cu")))["flash_decode_splitk_kernel"]
+    bad, _ = unwaited_returns(body)
+    assert not bad, f"flash_decode_splitk_kernel returns without waiting for the kernel before it: {bad}"
+    assert body.count("pdl_wait();") == 3  # at once without the early start; before a return; in the producer
