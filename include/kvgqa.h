@@ -390,7 +390,10 @@ kvgqa_status prefill_varlen_gqa_cached_rows_out_(const kvgqa_tensor* q, const kv
  * Device-side checks: a sequence whose query_starts, kv_lengths or number of new
  * tokens is out of range (negative or decreasing, past N, more new tokens than
  * cells or than max_query_len, more cells than the table or the mass has) sets
- * KVGQA_FLAG_POSITION_RANGE and is skipped: nothing of it is written.  A needed
+ * KVGQA_FLAG_POSITION_RANGE and is skipped: nothing of it is written.  Rows that
+ * several sequences claim, as they can where query_starts falls and rises again,
+ * have no meaning; where such sequences together pass the work that N rows can
+ * need, the attention and the mass set the flag and write nothing.  A needed
  * block_table entry outside [0, P) sets KVGQA_FLAG_PAGE_RANGE; no memory outside
  * the pool is touched, other sequences are unaffected, and of that sequence the
  * store skips the token, the eviction skips the sequence, and the attention's

@@ -48,10 +48,19 @@ struct PagedRange {
 };
 constexpr int kPagedSeqs = 32;  // sequences whose metadata a CTA keeps at hand
 
-// Called by the whole CTA of THREADS; units(seq) gives a sequence's units (their
-// sum below 2^30), scratch has THREADS / 32 + 2 ints and seqs kPagedSeqs entries
-// of shared memory.  False if nothing is left for this CTA.  Passes a barrier of
-// the CTA in either case (m.A > 0).
+// The host refuses calls whose units could reach this many, but counts every
+// packed row once.  Sequences whose rows overlap (query_starts that fall and rise
+// again) can pass it together, so sums of units stop there instead of wrapping;
+// one sequence's units are below it.
+constexpr int kPagedUnits = 1 << 30;
+__device__ __forceinline__ int add_units(int x, int y) {
+  return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), static_cast<unsigned>(kPagedUnits)));
+}
+
+// Called by the whole CTA of THREADS; units(seq) gives a sequence's units,
+// scratch has THREADS / 32 + 2 ints and seqs kPagedSeqs entries of shared memory.
+// False if nothing is left for this CTA, and for every CTA if the sequences have
+// kPagedUnits or more together.  Passes a barrier of the CTA in either case (m.A > 0).
 template <int THREADS, typename Units>
 __device__ bool paged_range(const PagedMeta& m, int32_t* status, int num_ctas, int min_units, int* scratch,
                             PagedSeq* seqs, PagedRange& r, Units units_of) {
@@ -75,21 +84,22 @@ __device__ bool paged_range(const PagedMeta& m, int32_t* status, int num_ctas, i
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      if (lane >= o) incl = add_units(incl, t);
     }
     if (chunk > 0) __syncthreads();  // the last chunk's sums have been read
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    excl = total + incl - units;
+    excl = add_units(total, incl - units);  // (exact unless the total reaches kPagedUnits)
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const int t = scratch[w];
-      if (w < warp) excl += t;
-      total += t;
+      if (w < warp) excl = add_units(excl, t);
+      total = add_units(total, t);
     }
   };
   for (int c = 0; c < chunks; ++c) scan(c);
-  if (blockIdx.x == 0 && bad) atomicOr(status, KVGQA_FLAG_POSITION_RANGE);
+  if (blockIdx.x == 0 && (bad || total >= kPagedUnits)) atomicOr(status, KVGQA_FLAG_POSITION_RANGE);
+  if (total >= kPagedUnits) return false;
   r.w = max((total + num_ctas - 1) / num_ctas, min_units);
   const long long v0 = static_cast<long long>(blockIdx.x) * r.w;
   if (v0 >= total) return false;
