@@ -667,6 +667,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
           int before = 0;
           if (lane == 0) before = atomic_add_acq_rel_gpu(count, 1);
           if (__shfl_sync(FULLMASK, before, 0) == b1 - b0) {
+            __syncwarp();  // (a shuffle orders no memory: lane 0's acquire becomes every lane's here)
             merge_small<D, F16>(p, walk.first, min(walk.ql << p.gp_shift, kSmallRows), walk.g, b0, b1);
             if (lane == 0) *count = 0;  // ready for the next call
           }
