@@ -81,7 +81,7 @@ paged_rope_kv_store_kernel(const __grid_constant__ PagedStoreParams p, int split
   constexpr int HALF = D / 2;
   constexpr int CH = D / 16;   // lanes that share a head: 8 pairs each
   constexpr int HL = 32 / CH;  // heads a warp covers at a time
-  __shared__ float2 cs_s[kWarps][HALF];
+  __shared__ __align__(16) float2 cs_s[kWarps][HALF];  // (cos, sin) of each pair, read two at a time
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   if (trigger) pdl_trigger();
