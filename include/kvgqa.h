@@ -116,7 +116,8 @@ typedef enum kvgqa_status {
   KVGQA_EWORKSPACE = 6,  /* workspace too small or misaligned */
   KVGQA_ECUDA = 7,       /* a CUDA runtime call failed (message has the CUDA error) */
   KVGQA_EUNSUPPORTED = 8, /* a legal shape this build has no kernel for (e.g. D = 96) */
-  KVGQA_EFULL = 9         /* slot table: no free cache row */
+  KVGQA_EFULL = 9,        /* slot table: no free cache row */
+  KVGQA_ENOMEM = 10       /* the host's memory ran out */
 } kvgqa_status;
 
 /* Bits of the device status word (first 4 bytes of every workspace). */

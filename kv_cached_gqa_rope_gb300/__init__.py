@@ -40,7 +40,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libkvgqa.so")
 
 KVGQA_BF16, KVGQA_I32, KVGQA_F32, KVGQA_U8, KVGQA_F16 = 1, 2, 3, 4, 5
 STATUS_NAMES = {0: "OK", 1: "EINVAL", 2: "EDTYPE", 3: "ELAYOUT", 4: "EDEVICE", 5: "EALIAS",
-                6: "EWORKSPACE", 7: "ECUDA", 8: "EUNSUPPORTED", 9: "EFULL"}
+                6: "EWORKSPACE", 7: "ECUDA", 8: "EUNSUPPORTED", 9: "EFULL", 10: "ENOMEM"}
 FLAG_POSITION_RANGE, FLAG_ROW_RANGE, FLAG_TIMEOUT, FLAG_PAGE_RANGE = 0x1, 0x2, 0x4, 0x8
 STATUS_BYTES = 256
 _DTYPES = {torch.bfloat16: KVGQA_BF16, torch.int32: KVGQA_I32, torch.float32: KVGQA_F32,

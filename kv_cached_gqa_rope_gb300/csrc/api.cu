@@ -14,6 +14,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
 
@@ -297,6 +298,13 @@ kvgqa_status guarded(F&& f) {
     return KVGQA_OK;
   } catch (const Fail& e) {
     return e.code;
+  } catch (const std::exception& e) {  // the host's memory: nothing else here throws
+    try {
+      g_last_error = e.what();
+    } catch (...) {
+      g_last_error.clear();
+    }
+    return KVGQA_ENOMEM;
   }
 }
 
