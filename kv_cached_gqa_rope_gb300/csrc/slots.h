@@ -19,9 +19,9 @@ class SlotTable {
  public:
   enum Reason { kStop = 0, kLength = 1, kCancel = 2 };
 
-  SlotTable(int num_slots, int max_seq) : max_seq_(max_seq), owner_(num_slots, -1), length_(num_slots, 0) {}
+  SlotTable(int num_slots, int max_seq) : max_seq_(max_seq), length_(num_slots, kFree) {}
 
-  int num_slots() const { return static_cast<int>(owner_.size()); }
+  int num_slots() const { return static_cast<int>(length_.size()); }
   int max_seq() const { return max_seq_; }
   int active() const { return static_cast<int>(row_of_.size()); }
 
@@ -32,10 +32,9 @@ class SlotTable {
     auto it = row_of_.find(request);
     if (it != row_of_.end()) return it->second;
     for (int r = 0; r < num_slots(); ++r) {
-      if (owner_[r] < 0) {
-        owner_[r] = request;
+      if (length_[r] == kFree) {
+        row_of_[request] = r;  // (before the row is taken: it may throw)
         length_[r] = prompt_len;
-        row_of_[request] = r;
         return r;
       }
     }
@@ -46,8 +45,7 @@ class SlotTable {
   bool release(int64_t request, Reason why) {
     auto it = row_of_.find(request);
     if (it == row_of_.end()) return false;
-    owner_[it->second] = -1;
-    length_[it->second] = 0;
+    length_[it->second] = kFree;
     row_of_.erase(it);
     ++released_[why];
     return true;
@@ -94,9 +92,9 @@ class SlotTable {
   }
 
  private:
+  static constexpr int kFree = -1;
   int max_seq_;
-  std::vector<int64_t> owner_;   // request owning each row, -1 when free
-  std::vector<int> length_;      // tokens held by each row
+  std::vector<int> length_;      // tokens held by each row, kFree when no request owns it
   std::map<int64_t, int> row_of_;
   long long released_[3] = {0, 0, 0};
 };
