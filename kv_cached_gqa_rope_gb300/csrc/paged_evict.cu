@@ -11,7 +11,10 @@
 // ascending order by counting: each warp owns a contiguous stripe, counts its
 // kept cells by ballots, and writes them from its prefix on.  The masses of up to
 // kCachedCells cells are read once and kept in shared memory; those of longer
-// sequences are read five times, from L2 after the first.
+// sequences are read five times, from L2 after the first.  Each sequence's own
+// length decides, however wide the caller's mass is (32 sequences of 1500-8191
+// cells in a mass of 65536 a row: 113 us, 119 when the width decided; the zeros
+// behind the kept masses are 8 of them).
 //
 // Kernel 2 moves K and V in place: one read and one write of each kept cell
 // that moves.  A kept cell's new place is never behind its old one, so in
@@ -25,7 +28,7 @@
 // cut to 2048 take 105 us.  The move, 86 of them, runs at 5.7 TB/s read and
 // written, 84 % of a copy's rate; the choice is a chain of latencies over a
 // head's cells (their load, three counts, two walks), which CTAs of 1024 threads
-// shorten from 19 to 17 us.  4 sequences cut to 256 cells take 6.6 us.
+// shorten from 19 to 17 us.  4 sequences cut to 256 cells take 6.8 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,28 +53,22 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+struct SelShared {
+  int hist[kBins];
+  int warp_gt[kSelWarps], warp_eq[kSelWarps];
+  uint32_t digit;
+  int need;
+};
+
+// The choice of one (sequence a, KV head g) of n cells, by the whole CTA.
+// CACHED: the masses of all its cells fit `cells`.
 template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
-  extern __shared__ float cells[];  // CACHED: the masses of all cells
-  __shared__ int hist[kBins];
-  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
-  __shared__ uint32_t sel_digit;
-  __shared__ int sel_need;
-  const int a = blockIdx.x / p.H_kv, g = blockIdx.x % p.H_kv;
+__device__ __forceinline__ void select_cells(const PagedEvictParams& p, int a, int g, int n, SelShared& sh, float* cells) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
   const size_t head = static_cast<size_t>(a) * p.H_kv + g;
   const float* mass = p.mass + head * p.mass_cells;
   float* mass_out = p.mass_out + head * p.mass_cells;
   int32_t* kept = p.kept + head * p.keep;
-  const int n = p.m.kv_lengths[a];
-  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-  __syncthreads();
-  if (n < 0 || n > p.m.max_cells) {
-    if (g == 0 && tid == 0) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
-    return;
-  }
   const int old = n - p.recent;
   if (n > p.keep) {
     // The masses are read once, and the first digits counted, while the table's
@@ -83,7 +80,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
       for (int i = tid; i < n; i += kSelThreads) {
         const float x = mass[i];
         cells[i] = x;
-        if (i < old) atomicAdd(&hist[order_key(x) >> 21], 1);
+        if (i < old) atomicAdd(&sh.hist[order_key(x) >> 21], 1);
       }
     }
     bool ok = entry >= 0;
@@ -127,7 +124,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
 #pragma unroll 4
         for (int i = tid; i < old; i += kSelThreads) {
           const uint32_t k = key_of(i);
-          if ((k & above) == thr) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+          if ((k & above) == thr) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1);
         }
         __syncthreads();
       }
@@ -137,8 +134,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
       int c[kShare], sum = 0;
 #pragma unroll
       for (int i = 0; i < kShare; ++i) {
-        sum += c[i] = hist[kBins - 1 - kShare * tid - i];
-        hist[kBins - 1 - kShare * tid - i] = 0;  // for the next digits
+        sum += c[i] = sh.hist[kBins - 1 - kShare * tid - i];
+        sh.hist[kBins - 1 - kShare * tid - i] = 0;  // for the next digits
       }
       int incl = sum;
 #pragma unroll
@@ -146,18 +143,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
         const int t = __shfl_up_sync(FULL, incl, o);
         if (lane >= o) incl += t;
       }
-      if (lane == 31) warp_gt[warp] = incl;
+      if (lane == 31) sh.warp_gt[warp] = incl;
       __syncthreads();
-      int before = incl - sum + __reduce_add_sync(FULL, lane < warp ? warp_gt[lane] : 0);
+      int before = incl - sum + __reduce_add_sync(FULL, lane < warp ? sh.warp_gt[lane] : 0);
       if (before < need && before + sum >= need) {
         int i = 0;
         while (before + c[i] < need) before += c[i++];
-        sel_digit = kBins - 1 - kShare * tid - i;
-        sel_need = need - before;
+        sh.digit = kBins - 1 - kShare * tid - i;
+        sh.need = need - before;
       }
       __syncthreads();
-      thr |= sel_digit << shift;
-      need = sel_need;
+      thr |= sh.digit << shift;
+      need = sh.need;
     }
   }
 
@@ -181,13 +178,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
     eqs += __popc(__ballot_sync(FULL, eq));
   }
   if (lane == 0) {
-    warp_gt[warp] = gts;
-    warp_eq[warp] = eqs;
+    sh.warp_gt[warp] = gts;
+    sh.warp_eq[warp] = eqs;
   }
   __syncthreads();
   // cells of the threshold's key before this stripe; kept cells before it
-  int eq_before = __reduce_add_sync(FULL, lane < warp ? warp_eq[lane] : 0);
-  int at = __reduce_add_sync(FULL, lane < warp ? warp_gt[lane] : 0) + min(eq_before, need);
+  int eq_before = __reduce_add_sync(FULL, lane < warp ? sh.warp_eq[lane] : 0);
+  int at = __reduce_add_sync(FULL, lane < warp ? sh.warp_gt[lane] : 0) + min(eq_before, need);
   for (int i = s0 + lane; i < s0 + S; i += 32) {
     bool gt, eq;
     classify(i, gt, eq);
@@ -203,6 +200,27 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
     at += __popc(tm);
     eq_before += __popc(eqm);
   }
+}
+
+// WIDE: the rows of the mass have room for longer sequences than `cells`.
+template <bool WIDE>
+__global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(const __grid_constant__ PagedEvictParams p) {
+  extern __shared__ float cells[];  // of min(mass_cells, kCachedCells) cells
+  __shared__ SelShared sh;
+  const int a = blockIdx.x / p.H_kv, g = blockIdx.x % p.H_kv;
+  pdl_wait();
+  pdl_trigger();
+  const int n = p.m.kv_lengths[a];
+  for (int i = threadIdx.x; i < kBins; i += kSelThreads) sh.hist[i] = 0;
+  __syncthreads();
+  if (n < 0 || n > p.m.max_cells) {
+    if (g == 0 && threadIdx.x == 0) atomicOr(p.status, KVGQA_FLAG_POSITION_RANGE);
+    return;
+  }
+  // The form goes by the sequence's own length: a server's mass is as wide as the
+  // longest context it allows for, whatever its sequences hold.
+  if (!WIDE || n <= kCachedCells) select_cells<true>(p, a, g, n, sh, cells);
+  else select_cells<false>(p, a, g, n, sh, cells);
 }
 
 constexpr int kMoveThreads = 256;
@@ -300,11 +318,10 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // The masses are kept in shared memory up to kCachedCells cells a row; longer rows are read from L2 in each pass.
-  const bool cached = p.mass_cells <= kCachedCells;
-  cfg.dynamicSmemBytes = cached ? static_cast<size_t>(p.mass_cells) * sizeof(uint32_t) : 0;
-  const cudaError_t e = cached ? cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<true>, p)
-                               : cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<false>, p);
+  cfg.dynamicSmemBytes = static_cast<size_t>(std::min(p.mass_cells, kCachedCells)) * sizeof(float);
+  // (without the longer form in the kernel 4 sequences take 6.8 us, with it 6.9)
+  const cudaError_t e = p.mass_cells > kCachedCells ? cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<true>, p)
+                                                    : cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<false>, p);
   if (e != cudaSuccess) return e;
   cfg.dynamicSmemBytes = 0;
   cfg.gridDim = dim3(static_cast<unsigned>(heads * 2 * slices));
