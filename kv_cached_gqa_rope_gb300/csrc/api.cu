@@ -1150,7 +1150,10 @@ kvgqa_status paged_evict_out_(const kvgqa_tensor* mass, const kvgqa_tensor* kv_l
     View vws = check_workspace(workspace, KVGQA_STATUS_BYTES);
     const std::initializer_list<const View*> all = {&vm, &pv.lengths, &pv.table, &vkc, &vvc, &vmo, &vk, &vn, &vws};
     check_no_alias({&vkc, &vvc, &vmo, &vk, &vn, &vws}, all);
-    check_device(all, current_device());
+    const int dev = current_device();
+    check_device(all, dev);
+    kvgqa::PagedLayout lay;
+    check_cuda(kvgqa::paged_attention_layout(dev, (int)D, &lay), "paged eviction set-up");
     if (A == 0) return;
     if (M < p.m.max_cells) p.m.max_cells = (int)M;
     p.mass = static_cast<const float*>(mass->data);
@@ -1161,6 +1164,7 @@ kvgqa_status paged_evict_out_(const kvgqa_tensor* mass, const kvgqa_tensor* kv_l
     p.new_lengths = static_cast<int32_t*>(new_lengths->data);
     p.status = static_cast<int32_t*>(workspace->data);
     p.H_kv = (int)H_kv; p.D = (int)D; p.keep = (int)keep; p.recent = (int)recent; p.mass_cells = (int)M;
+    p.num_sms = lay.num_ctas;
     check_cuda(kvgqa::launch_paged_evict(p, static_cast<cudaStream_t>(stream)), "paged_evict launch");
   });
 }

@@ -203,6 +203,7 @@ struct PagedEvictParams {
   int32_t* status;
   PagedMeta m;
   int H_kv, D, keep, recent, mass_cells;
+  int num_sms;
 };
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
 

@@ -28,7 +28,7 @@
 // cut to 2048 take 105 us.  The move, 86 of them, runs at 5.7 TB/s read and
 // written, 84 % of a copy's rate; the choice is a chain of latencies over a
 // head's cells (their load, three counts, two walks), which CTAs of 1024 threads
-// shorten from 19 to 17 us.  4 sequences cut to 256 cells take 6.8 us.
+// shorten from 19 to 17 us.  4 sequences cut to 256 cells take 6.6-6.8 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -224,10 +224,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) paged_evict_select_kernel(cons
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveCtas = 4;     // resident on an SM
 constexpr int kMoveBatch = 4;    // 16-byte chunks per thread and batch (32 sequences to 2048 cells: 105 us; 2 or 8 chunks 119)
 constexpr int kTablePages = 2048;  // pages of the table kept in shared memory (more are looked up in L2)
 
-__global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const __grid_constant__ PagedEvictParams p,
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) paged_evict_move_kernel(const __grid_constant__ PagedEvictParams p,
                                                                            int slices) {
   __shared__ int pages[kTablePages];
   int b = blockIdx.x;
@@ -302,12 +303,14 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_evict_move_kernel(const
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   const long long heads = static_cast<long long>(p.m.A) * p.H_kv;
   if (heads == 0) return cudaSuccess;
-  // Column slices until there are CTAs for several rounds of every SM, so that
+  // Column slices until there are CTAs for four rounds of the GPU, so that
   // sequences of different lengths even out: down to 64 bytes, and to one
-  // 32-byte sector where the heads are too few to fill the GPU once.
+  // 32-byte sector where the heads are too few to fill the GPU once.  (32 sequences
+  // of 8 heads: 105 us in slices of 64 bytes, longer in ones of 32 or 128.)
+  const long long round = static_cast<long long>(p.num_sms) * kMoveCtas;
   int slices = 1;
-  while (slices < p.D / 32 && heads * 2 * slices < 2400) slices *= 2;
-  if (heads * 2 * slices < 600) slices *= 2;
+  while (slices < p.D / 32 && heads * 2 * slices < 4 * round) slices *= 2;
+  if (heads * 2 * slices < round) slices *= 2;
   if (heads * 2 * slices > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -319,7 +322,7 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.dynamicSmemBytes = static_cast<size_t>(std::min(p.mass_cells, kCachedCells)) * sizeof(float);
-  // (without the longer form in the kernel 4 sequences take 6.8 us, with it 6.9)
+  // (without the longer form in the kernel 4 sequences take 6.78-6.81 us, with it 6.84-6.87)
   const cudaError_t e = p.mass_cells > kCachedCells ? cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<true>, p)
                                                     : cudaLaunchKernelEx(&cfg, paged_evict_select_kernel<false>, p);
   if (e != cudaSuccess) return e;
