@@ -400,7 +400,7 @@ kvgqa_status prefill_varlen_gqa_cached_rows_out_(const kvgqa_tensor* q, const kv
  * store skips the token, the eviction skips the sequence, and the attention's
  * rows or masses have no meaning.
  *
- * Limits of the calls with attention in them: D in {64, 128}, G <= 16.
+ * Limits: D in {64, 128}; G <= 16 where queries meet keys (attention, mass).
  */
 
 /* Workspace of paged_rope_kv_store_out_: the status block. */
@@ -419,7 +419,10 @@ kvgqa_status paged_rope_kv_store_workspace_size(size_t* bytes);
  * positions[axis_of_pair[i], n] * theta^(-2i/D).  One axis is ordinary RoPE; with
  * three (time, height, width) the patches of an image or a video share positions
  * that text never does, so a token's position and its cell are not tied: after
- * an eviction they differ for text too.
+ * an eviction they differ for text too.  Angles are reduced exactly; their cosines,
+ * sines and the turn are FP32, within 2^-22 (|x1| + |x2|) of the exact values before
+ * the one rounding to the storage type.  (rope_kv_store_out_ keeps more digits:
+ * where a pair nearly cancels, the two may differ in a value's last bits.)
  *
  *   q [N,H_q,D], k/v [N,H_kv,D] (each row contiguous; rows may lie further apart,
  *     by any multiple of 8 elements, as views of a fused projection do)
@@ -457,7 +460,7 @@ kvgqa_status paged_gqa_attention_workspace_size(int64_t H_q, int64_t H_kv, int64
  * of a prompt; a call takes any mix.  Scores, softmax and sums are FP32, the
  * weights enter the second product in the storage type, out is rounded once.
  * Cells behind a sequence's last one weigh nothing whatever they hold; the
- * sequence's own values have to be finite.
+ * sequence's own values, and its scores times log2(e) in FP32, have to be finite.
  *
  *   q_rot [N,H_q,D], k_cache/v_cache (read), scale finite
  *   out [N,H_q,D] (written), lse [N,H_q] float32 (written; may be NULL)

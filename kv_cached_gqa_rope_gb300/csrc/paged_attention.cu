@@ -40,12 +40,12 @@
 // end; warps without a row of the sequence skip the softmax.
 // What bounds it, as measured (32 query heads, 8 KV heads of 128, BF16):
 //   long contexts of single tokens by the stream of K and V: 8 sequences of 65536
-//   cells take 260-262 us, 6.7 TB/s, the rate of a copy; shorter ones by that and about
+//   cells take 260-263 us, 6.7 TB/s, the rate of a copy; shorter ones by that and about
 //   12 us of start and end that do not shrink with the cache: 32 sequences of up
-//   to 4095 cells 57 us, 4.7 TB/s; 4 of up to 500 cells 8.5 us, all latency
+//   to 4095 cells 57 us, 4.7 TB/s; 4 of up to 500 cells 8.5-8.7 us, all latency
 //   (schedule 2, first tile 1.2, softmax 1.1, P.V and its commit 1.6, epilogue 0.9);
 //   long chunks by the chain S -> softmax -> P.V of a tile beside the other
-//   tile's MMAs: 4 chunks of 2048 tokens after 6000-14000 cells 1070-1095 us, 1.34-1.36
+//   tile's MMAs: 4 chunks of 2048 tokens after 6000-14000 cells 1073-1099 us, 1.33-1.36
 //   PFLOP/s, a round of two tiles 3300 clocks of which the MMAs take 2048.
 //   Measured and not kept: every second or third pair of exponentials as a polynomial
 //   (chunks 1513-1970 us where 1304 without), four softmax warpgroups (spills,
@@ -142,7 +142,9 @@ __device__ __forceinline__ int block_tokens(const PagedAttentionParams& p) { ret
 // off / BN + 1 + ceil((b + 1) tokens / BN) of them, at least what they have, for
 // off cells before the new tokens: a form whose sums over blocks are closed.  A
 // last block's units are a multiple of a CTA's fewest, so that few short segments
-// are dealt whole, one to a CTA (4 requests of up to 500 cells: 8.5 us, cut 11.2).
+// are dealt whole, one to a CTA (4 requests of up to 500 cells: 8.5 us, cut 11.2; more
+// long segments than CTAs lose by it: 32 of up to 4095 cells in 8 heads 54.7 us, cut
+// 54.0, mixed steps of 28 sequences 92.4, cut 90.6).
 constexpr int kPair = 2;
 __device__ __forceinline__ int block_weight(const PagedAttentionParams& p, int ql, int b) {
   return (ql - b * block_tokens(p)) << p.gp_shift > BM ? kPair : 1;
