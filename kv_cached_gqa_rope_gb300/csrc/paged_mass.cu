@@ -278,12 +278,14 @@ paged_mass_kernel(const __grid_constant__ PagedMassParams p, const __grid_consta
     *abort_flag = 0;
     fence_mbar_init();
   }
+  pdl_wait();
+  // Not before the wait: a grid that holds tensor memory while it waits could keep
+  // it from the CTAs it waits for.
   if (warp == W_MMA) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
-  pdl_wait();
   pdl_trigger();  // the next kernel may set itself up on SMs that are done here
   PagedRange range;
   bool work = paged_range<THREADS>(p.m, p.status, p.num_ctas, 1, reinterpret_cast<int*>(smem + C::SCR_OFF),

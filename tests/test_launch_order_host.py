@@ -72,6 +72,14 @@ def test_every_path_waits(file, name):
     assert waited, f"{name} does not wait for the kernel before it on every path"
 
 
+@pytest.mark.parametrize("file,name", [x for x in KERNELS if "tmem_alloc(" in dict(kernels(source(x[0])))[x[1]]])
+def test_no_grid_holds_tensor_memory_while_it_waits(file, name):
+    """It could be what the CTAs it waits for still ask for.  (The decode step's
+    early start does: the kernel it waits for is its own store, which has none.)"""
+    body = dict(kernels(source(file)))[name]
+    assert "tmem_alloc(" not in body[:body.index("pdl_wait();")]
+
+
 def test_the_decode_step_s_early_start_waits():
     """Its attention waits in the producer warp, behind the tiles it loads early:
     a CTA without work has none, and waits before it returns."""
