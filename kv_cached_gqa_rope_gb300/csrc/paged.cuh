@@ -57,8 +57,13 @@ __device__ __forceinline__ int add_units(int x, int y) {
   return static_cast<int>(min(static_cast<unsigned>(x) + static_cast<unsigned>(y), static_cast<unsigned>(kPagedUnits)));
 }
 
+// The scratch of paged_range in shared memory: each warp's sum and the range's
+// first sequence with its prefix; in whole groups of 16 bytes.
+constexpr int paged_scratch_bytes(int threads) { return (threads / 32 + 2 + 3) / 4 * 16; }
+
 // Called by the whole CTA of THREADS; units(seq) gives a sequence's units,
-// scratch has THREADS / 32 + 2 ints and seqs kPagedSeqs entries of shared memory.
+// scratch has paged_scratch_bytes(THREADS) and seqs kPagedSeqs entries of shared
+// memory, which must not overlap: the entries are written while the scratch is read.
 // False if nothing is left for this CTA, and for every CTA if the sequences have
 // kPagedUnits or more together.  Passes a barrier of the CTA in either case (m.A > 0).
 template <int THREADS, typename Units>

@@ -143,6 +143,7 @@ struct ACfg {
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
   static constexpr int SMEM = FLAG_OFF + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(TE_OFF - ML_OFF >= paged_scratch_bytes(THREADS), "the schedule's scratch");
 };
 
 // One warp merges the parts b0 .. b1 of a block of `rows` <= 32 rows (read past

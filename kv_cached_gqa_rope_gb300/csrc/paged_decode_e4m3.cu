@@ -100,7 +100,7 @@ struct DCfg {
   static constexpr int RED_OFF = RQ_OFF + kSegs * NR * 4;       // [warpgroup][4 warps]: maxima and sums of its rows, exponent, flag
   static constexpr int RED = 4 * (2 * HR + 2) * 4;
   static constexpr int SCR_OFF = RED_OFF + 2 * RED;             // the schedule's scratch
-  static constexpr int SEQ_OFF = SCR_OFF + 64;
+  static constexpr int SEQ_OFF = SCR_OFF + paged_scratch_bytes(THREADS);
   static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * static_cast<int>(sizeof(PagedSeq));
   // k_full, k_empty, v_full, v_empty [STAGES], s_full, p_full, o_done [kBufs], q_full, q_empty, part_full [2],
   // scale_full, scale_empty [kTiles], v_land, drain [2]
@@ -113,6 +113,7 @@ struct DCfg {
   static constexpr int TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(QBUF % 1024 == 0 && PBUF % 1024 == 0 && TILE % 1024 == 0, "swizzled tiles need 1024-byte alignment");
   static_assert(SMEM <= 232448 && COLS <= 512, "shared and tensor memory");
+  static_assert(SEQ_OFF - SCR_OFF >= paged_scratch_bytes(THREADS), "the schedule's scratch");
 };
 
 // N columns of 32 lanes each.

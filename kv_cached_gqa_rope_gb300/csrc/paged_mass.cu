@@ -83,6 +83,7 @@ struct MCfg {
   static constexpr int FLAG_OFF = SLOT_OFF + 8;
   static constexpr int SMEM = FLAG_OFF + 16 + 1024;
   static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SEQ_OFF - SCR_OFF >= paged_scratch_bytes(THREADS), "the schedule's scratch");
 };
 
 // Column blocks of a sequence, and the units of its items: one per column
