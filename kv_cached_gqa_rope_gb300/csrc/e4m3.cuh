@@ -28,6 +28,10 @@ __device__ __forceinline__ float e4m3_scale(int e) { return __uint_as_float(stat
 __device__ __forceinline__ float e4m3_inverse(int e) {
   return __uint_as_float(max(static_cast<uint32_t>(254 - e) << 23, 0x00400000u));
 }
+// 2^k for k up to 127: subnormal below 2^-126, 0 below 2^-149.
+__device__ __forceinline__ float pow2(int k) {
+  return __uint_as_float(k >= -126 ? static_cast<uint32_t>(k + 127) << 23 : k >= -149 ? 1u << (k + 149) : 0u);
+}
 // The least byte from 1 to 254 whose scale times 448 = 1.75 * 2^8 holds `bound`; 0 for 0.
 __device__ __forceinline__ int e4m3_exponent(float bound) {
   const int e = static_cast<int>((__float_as_uint(bound) + 0x1fffffu) >> 23) - 8;

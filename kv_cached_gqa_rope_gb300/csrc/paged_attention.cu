@@ -224,10 +224,8 @@ __device__ __forceinline__ void merge_small(const PagedAttentionParams& p, int t
 // for 16-bit scores, 2180-3479 us; by integer operations 1960-2607; scores read twice, half a
 // row at a time, 2200-2600; the scales read before the scores are there 1762.
 constexpr int kPShift = 7;
-// 2^(e - 127 - kPShift), 0 where that is no normal number.
-__device__ __forceinline__ float value_scale(int e) {
-  return e > kPShift ? __uint_as_float(static_cast<uint32_t>(e - kPShift) << 23) : 0.f;
-}
+// What an accumulator of weights times 2^kPShift is in the scale of exponent e.
+__device__ __forceinline__ float value_scale(int e) { return pow2(e - 127 - kPShift); }
 // 2^(e - E) as two binary16 numbers, for e <= E; 0 for e = 0.
 __device__ __forceinline__ __half2 relative_scale(int e, int E) {
   const int d = E - e;

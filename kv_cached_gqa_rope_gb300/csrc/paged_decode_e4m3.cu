@@ -669,8 +669,7 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       }
       alive = alive && KVGQA_WAIT(&o_done[(t - 1) % kBufs], ((t - 1) / kBufs) & 1);
       named_bar_sync(bar_id, 128);
-      // 2^(v_ref - 127) / 2^kWeightShift, 0 where that is no normal number
-      const float of = v_ref > kWeightShift ? __uint_as_float(static_cast<uint32_t>(v_ref - kWeightShift) << 23) : 0.f;
+      const float of = pow2(v_ref - 127 - kWeightShift);
       tc_fence_after();
       const int rows = min(walk.ql << p.gp_shift, NR);
       const bool whole = walk.whole(), starts = walk.vlo >= walk.v0;
