@@ -13,21 +13,24 @@
 //   queries  two (BF16) or three (binary16) e4m3 parts, each 2^5 of the one before:
 //            a row times a power of two that brings its largest value to [2^7, 2^8),
 //            q = q0 + 2^-5 q1 (+ 2^-10 q2): exact from 2^-14 (2^-16) of the largest on
-//   weights  three (BF16) or four (binary16) e5m2 parts of the weight in binary16, each
-//            2^3 of the one before: a relative error of 2^-9, or of binary16's 2^-12.  e5m2 is
-//            the upper half of binary16, so a part is one addition, one mask and one
-//            subtraction for two rows.
-// A key's scale multiplies its score, a value's its weight (against the largest
-// exponent so far, as with the running maximum); both are one number to a thread.
+//   weights  three (BF16) or four (binary16) e5m2 parts of the product with the value's
+//            scale in binary16, each 2^3 of the one before: a relative error of binary16's
+//            2^-11, with three parts 2^-9 more.  e5m2 is the upper half of binary16, so a part
+//            is one addition, one mask and one subtraction for two rows.
+// A key's scale multiplies its score, a value's its weight; both are one number to a
+// thread.  A row has two bases: of its weights 2^x, whose sum is FP32, and of its
+// products 2^(x + e) of weight and value scale, which become binary16 and parts: with one
+// for the whole block, or against the largest scale, a large value that a row does not
+// see, or that weighs nothing in it, would push its other products below binary16.
 //
 // Work.  Segments (sequence, KV head) of key tiles lie in one space of units, of
 // which each CTA of the persistent grid takes an equal range (paged_walk.cuh); a segment cut
 // by a boundary leaves FP32 partials, merged by the CTA that finishes last.
 //   warps 0-7   softmax, one thread per key and half of the rows (a warpgroup each): FP32,
-//               the base of a row follows its maximum when that grew by 2^6, which a
+//               a row's bases follow its maxima when one of them grew by 2^6, which a
 //               vote of the warpgroup finds out; only then is the maximum itself reduced and
 //               the accumulator moved (tiles in turn instead, with a join of the two
-//               at each segment's end: 32 sequences of up to 4095 cells 60 us where this takes 46, the join 4 us);
+//               at each segment's end: 32 sequences of up to 4095 cells 60 us where this took 46, the join 4 us);
 //   warp 8      TMA of K, one box per page;
 //   warp 9      the same for V; zeroes the cells behind a sequence's last one;
 //   warp 10     tcgen05.mma of S^T, up to kBufs tiles ahead of the softmax; warp 14 of P.V (a
@@ -38,11 +41,13 @@
 //   warp 13     the scales of a tile to shared memory, some tiles ahead (their reads hang
 //               on the block table's, which the copies need not wait for).
 // What bounds it, as measured (8 KV heads of 128, BF16): long contexts by the stream of codes:
-//   8 sequences of 65536 cells, 64 query heads, take 137-138 us, 6.4 TB/s, 94 % of the
+//   8 sequences of 65536 cells, 64 query heads, take 141 us, 6.2 TB/s, 92 % of the
 //   rate of a copy (the 16-bit cache 263); shorter ones by that and by what does not shrink with
 //   the cache, start, first tiles and 2-2.5 us for a segment's end: 32 sequences of up to
-//   4095 cells, 32 query heads, 45-46 us, 2.9 TB/s (16 bits 57); 4 of up to 500 cells
-//   7.6-7.9 us, all latency.  Measured and not kept: a segment's end as 4 units, 343.7 us over five
+//   4095 cells, 32 query heads, 48.6-49 us, 2.7 TB/s (16 bits 57); 4 of up to 500 cells
+//   7.8-8.0 us, all latency.  With one base of the products for all rows, the largest
+//   scale so far, they took 138-139, 46 and 7.7 us, and lost what the comment above says.  Measured
+//   there and not kept: a segment's end as 4 units, 343.7 us over five
 //   decode steps where 2 take 347.3, but 16 sequences of up to 8000 cells 41.1 where 39.2; MMAs issued by
 //   single threads 72 and 251 us (operands that the compiler does not know to be uniform
 //   cost 150 clocks an MMA); a wait for the room of the weights before the scores 175;
@@ -72,13 +77,13 @@ constexpr int W_K = 8, W_V = 9, W_S = 10, W_Q = 11, W_MERGE = 12, W_SCALE = 13, 
 constexpr int kBufs = 4;        // tiles whose scores, and whose weights, have room
 constexpr int kTiles = 8;       // tiles whose scales are at hand
 constexpr int kSegs = 8;        // segments whose rows' scales are at hand
-constexpr int kWeightShift = 9; // weights are times 2^9: at most 2^15 with the base's lag
+constexpr int kWeightShift = 9; // products are times 2^9: at most 2^15 with the base's lag
 constexpr float kLag = 6.f;
 constexpr float kNone = -1e30f; // a row that has seen no cell: finite, so that no difference is NaN
 
 struct __align__(16) KeyScales {
   float k[8];  // the scale of the keys' cells 16 i ..
-  int v[8];    // the exponent byte of the values'
+  float v[8];  // the exponent byte of the values', -inf for a scale of zero
 };
 
 // NR: rows of a block, padded.
@@ -97,8 +102,8 @@ struct DCfg {
   static constexpr int P_OFF = Q_OFF + 2 * QBUF;                // the weights of kBufs tiles
   static constexpr int TS_OFF = P_OFF + kBufs * PBUF;
   static constexpr int RQ_OFF = TS_OFF + kTiles * static_cast<int>(sizeof(KeyScales));  // the rows' scales of kSegs segments
-  static constexpr int RED_OFF = RQ_OFF + kSegs * NR * 4;       // [warpgroup][4 warps]: maxima and sums of its rows, exponent, flag
-  static constexpr int RED = 4 * (2 * HR + 2) * 4;
+  static constexpr int RED_OFF = RQ_OFF + kSegs * NR * 4;       // [warpgroup][4 warps]: maxima of its rows' scores and products, sums, flag
+  static constexpr int RED = 4 * (3 * HR + 1) * 4;
   static constexpr int SCR_OFF = RED_OFF + 2 * RED;             // the schedule's scratch
   static constexpr int SEQ_OFF = SCR_OFF + paged_scratch_bytes(THREADS);
   static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * static_cast<int>(sizeof(PagedSeq));
@@ -327,7 +332,7 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       if (t >= kTiles && !KVGQA_WAIT(&scale_empty[t % kTiles], (t / kTiles - 1) & 1)) break;
       KeyScales& ks = scales[t % kTiles];
       if (lane < 8) ks.k[lane] = e4m3_scale(ex.e);
-      else if (lane < 16) ks.v[lane - 8] = ex.e;
+      else if (lane < 16) ks.v[lane - 8] = ex.e > 0 ? static_cast<float>(ex.e) : -INFINITY;
       __syncwarp();
       if (lane == 0) mbar_arrive(&scale_full[t % kTiles]);
     }
@@ -527,13 +532,14 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
     const int row0 = wg * HR;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_tm = tmem + lane_base + C::O_COL + row0;
-    float* red = reinterpret_cast<float*>(smem + C::RED_OFF + wg * C::RED);  // maxima [4][HR]
-    float* sums = red + 4 * HR;                                             // [4][HR]
-    int* red_e = reinterpret_cast<int*>(sums + 4 * HR);                     // [4]
-    int* red_ok = red_e + 4;                                                // [4]
+    float* red = reinterpret_cast<float*>(smem + C::RED_OFF + wg * C::RED);  // maxima of the scores [4][HR]
+    float* red_y = red + 4 * HR;                                            // and of the products' exponents [4][HR]
+    float* sums = red_y + 4 * HR;                                           // [4][HR]
+    int* red_ok = reinterpret_cast<int*>(sums + 4 * HR);                    // [4]
     const int bar_id = 1 + wg;
-    float m[HR], l[HR];
-    int v_ref = 0;
+    // Of each row: the base of its weights and their sum, and what the base of its
+    // products has more (a whole number).
+    float m[HR], l[HR], vb[HR];
     int t = 0;
     // A wait that gave up must not keep this warp from a barrier that the others of its
     // warpgroup come to: it goes on without effect until they leave together.
@@ -544,15 +550,15 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       for (int r = 0; r < HR; ++r) {
         m[r] = kNone;
         l[r] = 0.f;
+        vb[r] = 0.f;
       }
-      v_ref = 0;
       const float* rq = q_scale + seg % kSegs * NR + row0;
       for (int k = 0; k < parts; ++k, ++t) {
         const int j = walk.j_first + k, b = t % kBufs;
         alive = alive && KVGQA_WAIT(&s_full[b], (t / kBufs) & 1);
         bool grow = !alive;
         float x[HR];
-        int ev = 0;
+        float ev;  // the value's exponent
         tc_fence_after();
         {
           float s[C::QP][HR];
@@ -577,25 +583,28 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
 #pragma unroll
           for (int r = 0; r < HR; ++r)
             if (cell > min(walk.off + ((row0 + r) >> p.gp_shift), walk.kend - 1)) x[r] = -INFINITY;
-          if (cell >= walk.kend) ev = 0;
         }
 #pragma unroll
-        for (int r = 0; r < HR; ++r) grow = grow || x[r] - m[r] > kLag;
-        grow = grow || ev > v_ref;
+        for (int r = 0; r < HR; ++r) {
+          const float t = x[r] - m[r];
+          grow = grow || fmaxf(t, t + (ev - vb[r])) > kLag;
+        }
         if (vote_any(bar_id, grow)) {
           // The maxima of the tile, over the warpgroup.
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
-            float v = x[r];
+            float v = x[r], y = x[r] + ev;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULLMASK, v, o));
-            if (lane == 0) red[quarter * HR + r] = v;
+            for (int o = 16; o; o >>= 1) {
+              v = fmaxf(v, __shfl_xor_sync(FULLMASK, v, o));
+              y = fmaxf(y, __shfl_xor_sync(FULLMASK, y, o));
+            }
+            if (lane == 0) {
+              red[quarter * HR + r] = v;
+              red_y[quarter * HR + r] = y;
+            }
           }
-          const int we = __reduce_max_sync(FULLMASK, ev);
-          if (lane == 0) {
-            red_e[quarter] = we;
-            red_ok[quarter] = alive;
-          }
+          if (lane == 0) red_ok[quarter] = alive;
           // The accumulator is moved behind the P.V of its last tile.
           const bool move = k > 0;
           if (move) alive = alive && KVGQA_WAIT(&o_done[(t - 1) % kBufs], ((t - 1) / kBufs) & 1);
@@ -604,18 +613,20 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
             gone = true;
             break;
           }
-          const int e_new = max(max(max(red_e[0], red_e[1]), max(red_e[2], red_e[3])), v_ref);
-          const float e_move = ex2(static_cast<float>(v_ref - e_new));
-          v_ref = e_new;
           float alpha[HR];
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
             const float top = fmaxf(fmaxf(red[r], red[HR + r]), fmaxf(red[2 * HR + r], red[3 * HR + r]));
-            const float to = fmaxf(m[r], top);
-            const float a = ex2(m[r] - to);
+            const float top_y = fmaxf(fmaxf(red_y[r], red_y[HR + r]), fmaxf(red_y[2 * HR + r], red_y[3 * HR + r]));
+            // (A row that has seen no cell, or none with a scale, has a base near kNone, and
+            // zeros so far.  The products' base falls by less than a binade where the
+            // weights' alone grows, else it does not fall; as the latter is a maximum here, the
+            // difference is 254 at most.)
+            const float to = fmaxf(m[r], top), by = floorf(fmaxf(m[r] + vb[r], top_y) - to), a = m[r] - to;
+            alpha[r] = ex2(fminf(a + (vb[r] - by), 1.f));
+            l[r] *= ex2(a);
             m[r] = to;
-            l[r] *= a;
-            alpha[r] = a * e_move;
+            vb[r] = by;
           }
           if (move) {
             tc_fence_after();
@@ -631,18 +642,15 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
             tmem_wait_st();
           }
         }
-        // The weights: exp2(x - m), and times the value's scale in their parts.  (The
-        // factor is 0 for a scale of zero, and where it would be no normal number.)
-        const int ve = ev - v_ref + kWeightShift + 127;
-        const float vf = ev > 0 && ve > 0 ? __uint_as_float(static_cast<uint32_t>(ve) << 23) : 0.f;
+        // The weights: exp2(x - m), and times the value's scale in their parts.
         const uint32_t pb = sbase + C::P_OFF + b * C::PBUF + (key & 15);
         if (t >= kBufs) alive = alive && KVGQA_WAIT(&o_done[b], (t / kBufs - 1) & 1);  // the buffer's last weights have been used
 #pragma unroll
         for (int r = 0; r < HR; r += 2) {
-          const float p0 = ex2(x[r] - m[r]), p1 = ex2(x[r + 1] - m[r + 1]);
-          l[r] += p0;
-          l[r + 1] += p1;
-          __half2 h = __floats2half2_rn(p0 * vf, p1 * vf);
+          const float t0 = x[r] - m[r], t1 = x[r + 1] - m[r + 1];
+          l[r] += ex2(t0);
+          l[r + 1] += ex2(t1);
+          __half2 h = __floats2half2_rn(ex2(t0 + (ev - vb[r] + kWeightShift)), ex2(t1 + (ev - vb[r + 1] + kWeightShift)));
 #pragma unroll
           for (int part = 0; part < C::PP; ++part) {
             const uint32_t c = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
@@ -669,7 +677,6 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       }
       alive = alive && KVGQA_WAIT(&o_done[(t - 1) % kBufs], ((t - 1) / kBufs) & 1);
       named_bar_sync(bar_id, 128);
-      const float of = pow2(v_ref - 127 - kWeightShift);
       tc_fence_after();
       const int rows = min(walk.ql << p.gp_shift, NR);
       const bool whole = walk.whole(), starts = walk.vlo >= walk.v0;
@@ -688,7 +695,8 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
 #pragma unroll
       for (int r = 0; r < HR; ++r) {
         l[r] = sums[r] + sums[HR + r] + sums[2 * HR + r] + sums[3 * HR + r];
-        o[r] *= of;
+        // (the products' base in two steps: by itself it may be below FP32's range)
+        o[r] = o[r] * pow2(-kWeightShift) * pow2(static_cast<int>(fmaxf(vb[r], -1000.f)) - 127);
       }
       if (alive) {
 #pragma unroll
