@@ -593,10 +593,9 @@ kvgqa_status paged_gqa_attention_e4m3_workspace_size(int64_t H_q, int64_t H_kv, 
  * stand for.  Roundings of its own: a query's values below 2^-9 (BF16) or 2^-6 (FP16)
  * of the largest of its head are held to 2^-17 of that; a weight enters the second
  * product together with its value's scale, off by a relative 2^-9 + 2^-11 (BF16) or 2^-11
- * (FP16) at most, and by 2^-31 of the largest such product of its row; and where a
- * sequence has more tokens than a small block holds, values whose scale is below 2^-15 of
- * the largest in their 128 cells, seen or not, are held to 2^-25 of that, and products
- * to 2^-32 of what the largest weight and the largest scale would give.
+ * (FP16) at most, and by 2^-31 of the largest such product of its row.  (BF16 calls hold
+ * them to 2^-11 where a sequence has more tokens than a small block holds.)  Cells that a row
+ * does not see change nothing in it.
  *
  *   q_rot [N,H_q,D] bf16, k_cache/v_cache e4m3, k_scale/v_scale uint8 (read)
  *   out [N,H_q,D] bf16 (written), lse [N,H_q] float32 (written; may be NULL)

@@ -100,8 +100,7 @@ __host__ __device__ constexpr size_t slot_floats(int D) { return static_cast<siz
 // What the softmax has to know of a tile of codes.
 struct __align__(16) TileScales {
   float k[8];  // the scale of the keys' cells 16 i ..
-  int v;       // the largest exponent byte of the values
-  int pad[3];
+  float v[8];  // the exponent byte of the values', -inf for a scale of zero
 };
 
 // SMALL: no block of the call has more than kSmallRows rows (decode steps, a
@@ -204,42 +203,41 @@ __device__ __forceinline__ void merge_small(const PagedAttentionParams& p, int t
 // columns.
 //
 // The weights would lose too much in 8 bits, so the values become binary16 on their
-// way, in which a code is exact and one instruction expands two: with the largest
-// exponent E of a tile (128 cells) a value is code * 2^(e - E), e its block's; exact
-// down to scales of 2^-15 of the largest, from where on it is rounded to 2^-24.
-// 2^(E - 127) goes into the weights' exponents, against the largest E so far (the
-// accumulator moves when that grows).  Weights are times 2^kPShift, at most 2^15 (the base
-// follows the maximum when it grew by 2^8), which leaves 2^-32 as their largest error.
+// way, in which a code is exact and one instruction expands two.  The values' scales, one
+// for each 16 columns, go into the weights' exponents: the product 2^(x + e) of a weight and
+// a scale becomes binary16, against a base of its own in each row, at most 2^15 (the base
+// follows the row's largest product when that grew by 2^8), 2^kPShift at least.  2^-32 of the
+// largest product is the largest error of the others.  (With one base for a block of rows, or
+// values relative to a tile's largest scale, a large value that a row does not see, or that
+// weighs nothing in it, would push its other products below binary16.)  The sum of the weights
+// takes the scales out again, in FP32.
 //
-// What bounds it: 4 chunks of 2048 tokens after 6000-14000 cells take 1710-1730 us, 0.85
-// PFLOP/s, where the 16-bit cache takes 1105: a round of two tiles 5200 clocks, of which the
-// MMAs take 2048, the softmax of a tile 2500 (16 bits: 1500; its scales are 8 more
-// registers and reads of shared memory, and the code of four roles passes through
-// the instruction cache) and the four expanding warps 1700, beside it.  A tile of a block with one query
-// tile takes 2.1 us, one with two 2.7.  As V lands in stages of its own, a copy's
+// What bounds it: 4 chunks of 2048 tokens after 6000-14000 cells take 1800 us, 0.81
+// PFLOP/s, where the 16-bit cache takes 1105, a mixed step of 28 sequences 148 (98): the
+// softmax of a tile beside the MMAs, 2048 clocks of a round of two tiles (its scales are
+// more registers, exponentials and reads of shared memory, and the code of four roles passes
+// through the instruction cache), and the four expanding warps beside it.  Before the values'
+// scales went into the weights it was 1736 and 153: a round 5200 clocks, the softmax of a tile
+// 2500 (16 bits: 1500), the expansion 1700; a tile of a block with one query tile took 2.1
+// us, one with two 2.7.  As V lands in stages of its own, a copy's
 // latency is not in the chain of P.V, expansion, P.V: landing in the upper half of the expanded
-// stage and expanding in place it takes 2.5 and 2.8 us, 163 us for a mixed step of 28
-// sequences where this took 156.  Measured and not kept: a timing run whose values are not
+// stage and expanding in place it took 2.5 and 2.8 us, 163 us for a mixed step of 28
+// sequences where this took 156.  Measured there and not kept: a timing run whose values are not
 // expanded at all takes 2.8 % less with two query tiles, 23 % with one; expanding K too,
 // for 16-bit scores, 2180-3479 us; by integer operations 1960-2607; scores read twice, half a
 // row at a time, 2200-2600; the scales read before the scores are there 1762.
 constexpr int kPShift = 7;
-// What an accumulator of weights times 2^kPShift is in the scale of exponent e.
-__device__ __forceinline__ float value_scale(int e) { return pow2(e - 127 - kPShift); }
-// 2^(e - E) as two binary16 numbers, for e <= E; 0 for e = 0.
-__device__ __forceinline__ __half2 relative_scale(int e, int E) {
-  const int d = E - e;
-  const uint32_t b = e == 0 || d > 24 ? 0u : d < 15 ? static_cast<uint32_t>(15 - d) << 10 : 1u << (24 - d);
-  const uint32_t w = b | b << 16;
-  return *reinterpret_cast<const __half2*>(&w);
+// A row's products are in this times its accumulator, where their base has `vb` more than
+// the weights' (254 at most).
+__device__ __forceinline__ float value_scale(float vb) {
+  return pow2(static_cast<int>(fmaxf(vb, -1000.f)) - 127 - kPShift);
 }
 
 // One warp of the four that expand a tile of codes: cells 32 * part .. + 31, from `raw`
 // to the stage `st`.  Its codes in registers, `took` frees the one and waits for
 // the other.  Cells from `live` on become zero.
 template <int D, typename Took>
-__device__ __forceinline__ bool expand_codes(uint32_t raw, uint32_t st, int part, int lane, int exps, int first_lane,
-                                             int largest, int live, const Took& took) {
+__device__ __forceinline__ bool expand_codes(uint32_t raw, uint32_t st, int part, int lane, int live, const Took& took) {
   using Tile = PagedTile<D>;
   constexpr int HALVES = Tile::HALVES;
   const int row = lane >> 3, c = lane & 7;  // a cell of 4, and 8 of its values in each half of a head
@@ -253,8 +251,6 @@ __device__ __forceinline__ bool expand_codes(uint32_t raw, uint32_t st, int part
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) x[b][h] = lds64(codes + b * 4 * D + (h ^ first) * 64);
   }
-  const __half2 f[2] = {relative_scale(__shfl_sync(FULLMASK, exps, first_lane + part * 2), largest),
-                        relative_scale(__shfl_sync(FULLMASK, exps, first_lane + part * 2 + 1), largest)};
   if (!took()) return false;
   // Cells row and row + 4 of the groups of 8.
   const uint32_t to = st + part * 4 * Tile::GROUP + row * 128;
@@ -264,8 +260,7 @@ __device__ __forceinline__ bool expand_codes(uint32_t raw, uint32_t st, int part
     const bool gone = part * 32 + b * 4 + row >= live;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
-      const __half2 v[4] = {__hmul2(e4m3_half2(x[b][h].x), f[b >> 2]), __hmul2(e4m3_half2(x[b][h].x >> 16), f[b >> 2]),
-                            __hmul2(e4m3_half2(x[b][h].y), f[b >> 2]), __hmul2(e4m3_half2(x[b][h].y >> 16), f[b >> 2])};
+      const __half2 v[4] = {e4m3_half2(x[b][h].x), e4m3_half2(x[b][h].x >> 16), e4m3_half2(x[b][h].y), e4m3_half2(x[b][h].y >> 16)};
       uint4 w = *reinterpret_cast<const uint4*>(v);
       if (gone) w = make_uint4(0, 0, 0, 0);
       sts128(to + (b >> 1) * Tile::GROUP + (h ^ first) * 1024 + chunk[b & 1], w);
@@ -474,9 +469,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       const int group = t.group(walk, lane);
       if (kE4M3) {
         TileScales& ts = tile_scales[it & (C::kTiles - 1)];
-        const int ev = __reduce_max_sync(FULLMASK, lane < 8 ? 0 : ex.e);
         if (lane < 8) ts.k[lane] = e4m3_scale(ex.e);
-        if (lane == 8) ts.v = ev;
+        else if (lane < 16) ts.v[lane - 8] = ex.e > 0 ? static_cast<float>(ex.e) : -INFINITY;
         __syncwarp();  // (the arrival below publishes them)
       }
       if (lane == 0) mbar_arrive_expect_tx(&k_full[s], t.n * t.rows * D * (kE4M3 ? 1 : 2));
@@ -549,7 +543,6 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     const int part = warp - W_EXPAND;
     float* q_scale = reinterpret_cast<float*>(smem + C::QS_OFF);
     int it = 0, seg = 0, qn[2] = {0, 0};
-    TileExponents ex;
     auto publish = [&](uint64_t* bar) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -558,7 +551,6 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     bool ok = true;
     for (; walk.ok; walk.advance(), ++it) {
       if (walk.fresh()) {
-        ex.start(walk, lane);
         for (int x = 0; x < (walk.dual() ? 2 : 1) && ok; ++x) {
           const int i = walk.dual() ? x : walk.slot;
           ok = KVGQA_WAIT(&q_full[i], (i == 0 ? qn[0] : qn[1]) & 1);
@@ -573,11 +565,9 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         if (!ok) break;
         ++seg;
       }
-      ex.advance(walk, lane);
-      const int ev = __reduce_max_sync(FULLMASK, lane < 8 ? 0 : ex.e);
       const int sr = it % C::NR, sv = it % C::NV;
       if (!KVGQA_WAIT(&raw_full[sr], (it / C::NR) & 1) ||
-          !expand_codes<D>(sbase + C::R_OFF + sr * C::KTILE, sbase + C::V_OFF + sv * C::TILE, part, lane, ex.e, 8, ev,
+          !expand_codes<D>(sbase + C::R_OFF + sr * C::KTILE, sbase + C::V_OFF + sv * C::TILE, part, lane,
                            walk.kend - walk.j * BN, [&]() -> bool {
                              __syncwarp();
                              if (lane == 0) mbar_arrive(&raw_empty[sr]);
@@ -744,7 +734,8 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
     const float ce = c > 0.f ? c : 1.f;
     float m_ref = -INFINITY, l = 0.f;
     float row_c = c;         // codes: the scale with the query row's
-    int v_ref = 0, seg = 0;  // codes: the largest exponent of the values so far; segments so far
+    float vb = 0.f;          // codes: what the base of the products has more than the weights' (a whole number)
+    int seg = 0;             // codes: segments so far
     float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
     int t = 0, t_other = 0;  // tiles of this group and of the other so far
     int n_shared = 0;        // shared parts so far
@@ -769,17 +760,16 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       if (!ok) break;
       if (live) {
       tc_fence_after();
-      int v_exp = 0;
       float cb[8];  // codes: the scores' scale in each 16 columns
+      float yt = 0.f;  // codes: the largest exponent of a product
+      const TileScales& ts = tile_scales[(walk.ring + j - walk.j_first) & (C::kTiles - 1)];
       if constexpr (kE4M3) {
-        const TileScales& ts = tile_scales[(walk.ring + j - walk.j_first) & (C::kTiles - 1)];
         if (first)
           row_c = fabsf(c) * reinterpret_cast<const float*>(smem + C::QS_OFF)[((seg_now & (C::kSegs - 1)) * 2 + (dual ? x : 0)) * BM + r];
         const float4 k0 = *reinterpret_cast<const float4*>(ts.k), k1 = *reinterpret_cast<const float4*>(ts.k + 4);
         const float ks[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int b = 0; b < 8; ++b) cb[b] = fmaxf(row_c * ks[b], 1.2e-38f);  // (hidden scores are -inf: not times zero)
-        v_exp = ts.v;
       }
       // Scores enter the softmax as s * ce with ce > 0 (a scale that is not
       // positive is folded into the scores first).
@@ -806,6 +796,9 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
                                 fmax3(sb[9], sb[10], sb[11]), fmax3(fmax3(sb[12], sb[13], sb[14]), sb[15], sb[15]));
         }
         mt = fmax3(fmax3(mb[0], mb[1], mb[2]), fmax3(mb[3], mb[4], mb[5]), fmaxf(mb[6], mb[7]));
+        const float4 v0 = *reinterpret_cast<const float4*>(ts.v), v1 = *reinterpret_cast<const float4*>(ts.v + 4);
+        yt = fmax3(fmax3(mb[0] + v0.x, mb[1] + v0.y, mb[2] + v0.z), fmax3(mb[3] + v0.w, mb[4] + v1.x, mb[5] + v1.y),
+                   fmaxf(mb[6] + v1.z, mb[7] + v1.w));
       } else {
         float mx[8];
 #pragma unroll
@@ -818,26 +811,28 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         const float mraw = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         mt = mraw * ce;
       }
-      const bool grow = first || mt > m_ref + 8.f;   // keep the old base unless it grew by 2^8
-      float alpha = 1.f;
+      // Keep the old base unless it grew by 2^8.
+      const bool grow = first || mt > m_ref + 8.f || (kE4M3 && yt > m_ref + vb + 8.f);
+      float alpha = 1.f;  // of the accumulator
       if (grow) {
-        alpha = first ? 0.f : ex2(m_ref - mt);
-        m_ref = mt;
-        l = first ? 0.f : l * alpha;  // (the last segment's row may have been padding, its sum anything)
-      }
-      // Codes: the weights take the values' scale against the largest so far.
-      float shift = 0.f, unshift = 1.f;
-      bool v_grow = false;
-      if constexpr (kE4M3) {
-        v_grow = !first && v_exp > v_ref;
-        if (v_grow) alpha *= ex2(static_cast<float>(v_ref - v_exp));
-        if (first || v_exp > v_ref) v_ref = v_exp;
-        shift = static_cast<float>(max(v_exp - v_ref, -100) + kPShift);  // (2^-100 of a weight is no binary16 number anyway)
-        unshift = ex2(-shift);
+        const float to = kE4M3 && !first ? fmaxf(m_ref, mt) : mt;
+        const float al = first ? 0.f : ex2(m_ref - to);  // of the sum
+        alpha = al;
+        if constexpr (kE4M3) {
+          // (A row that has seen no cell with a scale has a base near -1e30, and zeros so far.
+          // The products' base falls by less than a binade where the weights' alone grows,
+          // else it does not fall; as the latter is a maximum here, the difference is 254
+          // at most.)
+          const float by = fmaxf(floorf((first ? yt : fmaxf(m_ref + vb, yt)) - to), -1e30f);
+          alpha = first ? 0.f : ex2(fminf(m_ref - to + (vb - by), 1.f));
+          vb = by;
+        }
+        m_ref = to;
+        l = first ? 0.f : l * al;  // (the last segment's row may have been padding, its sum anything)
       }
       // S_x of this tile being ready means the P.V of the previous tile is
       // complete, so O_x may be rescaled here without a further wait.
-      if (__any_sync(FULLMASK, (grow && !first) || v_grow)) {
+      if (__any_sync(FULLMASK, grow && !first)) {
 #pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           uint32_t w[32];
@@ -851,24 +846,42 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       // A row that has seen no cell yet (the part of a cut segment may begin
       // in tiles that only later tokens see) keeps the base -inf; its weights
       // are 2^(-inf - 0) = 0.
-      const float base = (m_ref == -INFINITY ? 0.f : -m_ref) + (kE4M3 ? shift : 0.f);
+      const float base = m_ref == -INFINITY ? 0.f : -m_ref;
       float2 ls = make_float2(0.f, 0.f);
       const float2 c2 = make_float2(ce, ce), nm2 = make_float2(base, base);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
+        if constexpr (kE4M3) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int i0 = half * 64 + 2 * e;
-          const float2 xx = ffma2(make_float2(sv[i0], sv[i0 + 1]), kE4M3 ? make_float2(cb[i0 >> 4], cb[i0 >> 4]) : c2, nm2);
-          const float2 pr = make_float2(ex2(xx.x), ex2(xx.y));
-          ls = fadd2(ls, pr);
-          w[e] = kE4M3 ? Elem<true>::pack2(pr.x, pr.y) : E::pack2(pr.x, pr.y);
+          for (int b = half * 4; b < half * 4 + 4; ++b) {
+            // (2^-100 of a weight is no binary16 number anyway)
+            const float shift = fmaxf(ts.v[b] - vb, -100.f) + kPShift, by = base + shift;
+            float2 lb = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 xx = ffma2(make_float2(sv[16 * b + 2 * e], sv[16 * b + 2 * e + 1]), make_float2(cb[b], cb[b]), make_float2(by, by));
+              const float2 pr = make_float2(ex2(xx.x), ex2(xx.y));
+              lb = fadd2(lb, pr);
+              w[(b - half * 4) * 8 + e] = Elem<true>::pack2(pr.x, pr.y);
+            }
+            const float unshift = ex2(-shift);
+            ls = ffma2(lb, make_float2(unshift, unshift), ls);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int i0 = half * 64 + 2 * e;
+            const float2 xx = ffma2(make_float2(sv[i0], sv[i0 + 1]), c2, nm2);
+            const float2 pr = make_float2(ex2(xx.x), ex2(xx.y));
+            ls = fadd2(ls, pr);
+            w[e] = E::pack2(pr.x, pr.y);
+          }
         }
         tmem_st32(s_col + half * 32, w);
       }
       tmem_wait_st();
-      l += kE4M3 ? (ls.x + ls.y) * unshift : ls.x + ls.y;
+      l += ls.x + ls.y;
       }
       // Each warp arrives once: every lane's TMEM stores are complete and
       // fenced before the warp synchronises, then lane 0 arrives.
@@ -886,13 +899,13 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
       const bool shared = !dual && walk.parts() > 1;
       t_other += dual ? walk.parts() : (walk.parts() + (walk.group() != x)) / 2;
       if (first) continue;  // no tile of this part was this group's
-      float wa = kE4M3 ? value_scale(v_ref) : 1.f, wb = 0.f;  // weights of the two accumulators
+      float wa = kE4M3 ? value_scale(vb) : 1.f, wb = 0.f;  // weights of the two accumulators
       if (shared) {
         const int ph = n_shared++ & 1;
         if (x == 1) {
           ml[r] = m_ref;
           ml[BM + r] = l;
-          if (kE4M3) ml[2 * BM + r] = value_scale(v_ref);
+          if (kE4M3) ml[2 * BM + r] = value_scale(vb);
           __syncwarp();
           if (lane == 0) mbar_arrive(ml_full);
           if (!__all_sync(FULLMASK, mbar_wait_bounded(ml_done, ph, abort_flag, p.status))) break;
@@ -909,7 +922,7 @@ paged_attention_kernel(const __grid_constant__ PagedAttentionParams p, const __g
         l = l * wa + lb * wb;
         m_ref = m;
         if (kE4M3) {
-          wa *= value_scale(v_ref);
+          wa *= value_scale(vb);
           wb *= ml[2 * BM + r];
         }
       }

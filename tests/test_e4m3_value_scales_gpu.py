@@ -12,8 +12,9 @@ pytestmark = pytest.mark.gpu
 
 BF, HF = torch.bfloat16, torch.float16
 GAPS = [(BF, 20), (BF, 34), (BF, 60), (HF, 20), (HF, 24)]
-TOKENS = [1, 3]
-LATER = [(4, 322, 2, 128), (4, 386, 2, 64), (8, 130, 4, 64), (16, 50, 1, 128)]
+TOKENS = [1, 3, 40]
+LATER = [(4, 322, 2, 128), (4, 386, 2, 64), (8, 130, 4, 64), (16, 50, 1, 128),
+         (40, 322, 4, 128), (40, 386, 4, 64), (150, 258, 2, 64), (300, 338, 2, 128)]
 
 
 def run(p):
