@@ -14,7 +14,7 @@
 //
 // Work.  A block's new cells have to be seen together, so a run (the new tokens of
 // one block, 16 at most) is one CTA's.  A CTA looks at `chunk` packed tokens (1 or
-// 16) and takes the runs that begin there.  It evaluates the run's angles once
+// 16, see the launch) and takes the runs that begin there.  It evaluates the run's angles once
 // for all heads into shared memory; a warp then takes a KV head's keys or values
 // of the whole run (D / 16 lanes to a token, so that its reads and codes stay in
 // registers between the bound and the rounding) and its share of the queries.  A
@@ -379,11 +379,15 @@ cudaError_t launch(const PagedStoreParams& p, cudaStream_t stream) {
   int ctas = 0;
   const cudaError_t e = resident_ctas<D, F16>(&ctas);
   if (e != cudaSuccess) return e;
-  // A CTA for every token where they are resident together or sequences have few, else
-  // one for every 16.  Measured, for every token and for every 16: 256 and 2048 sequences of one
-  // token 4.8 and 38, 27 and 41 us; 512 of 1-8 22 and 33; 64 of 16-64 22.8 and 22.7; 5 of
-  // 301-1237 13.6 and 9.7; 16 of 1021-1024 100 and 73.
-  const bool single = p.m.N <= ctas || p.m.N < 16ll * p.m.A;
+  // A CTA for every token where they are resident together or sequences have 256 at most
+  // in the mean, else one for every 16, whose runs go one after another: it costs most where
+  // single tokens stand beside a prompt.  Measured, for every token and for every 16: 256 and 2048
+  // sequences of one token 4.8 and 38, 27 and 41 us; 512 of 1-8 22 and 33; 63 single tokens
+  // and one prompt of 1100 17 and 40, 22 and six of 40-512 18 and 35, 15 and one of 2048 20 and 40;
+  // 32 of 24 15 and 21, of 64 20 and 19, of 128 32 and 27; 16 of 256 32 and 26; 5 of 301-1237 13.6
+  // and 9.7; 16 of 1021-1024 97-100 and 72, 74 with 16 single tokens beside them; against
+  // the rule 7 single tokens beside one prompt of 2048 19 and 30.
+  const bool single = p.m.N <= ctas || p.m.N < 256ll * p.m.A;
   const int chunk = single ? 1 : kScaleCells;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
