@@ -41,14 +41,18 @@
 //   warp 13     the scales of a tile to shared memory, some tiles ahead (their reads hang
 //               on the block table's, which the copies need not wait for).
 // What bounds it, as measured (8 KV heads of 128, BF16): long contexts by the stream of codes:
-//   8 sequences of 65536 cells, 64 query heads, take 141 us, 6.2 TB/s, 92 % of the
+//   8 sequences of 65536 cells, 64 query heads, take 140 us, 6.3 TB/s, 92 % of the
 //   rate of a copy (the 16-bit cache 263); shorter ones by that and by what does not shrink with
 //   the cache, start, first tiles and 2-2.5 us for a segment's end: 32 sequences of up to
-//   4095 cells, 32 query heads, 48.6-49 us, 2.7 TB/s (16 bits 57); 4 of up to 500 cells
-//   7.8-8.0 us, all latency.  With one base of the products for all rows, the largest
-//   scale so far, they took 138-139, 46 and 7.7 us, and lost what the comment above says.  Measured
-//   there and not kept: a segment's end as 4 units, 343.7 us over five
-//   decode steps where 2 take 347.3, but 16 sequences of up to 8000 cells 41.1 where 39.2; MMAs issued by
+//   4095 cells, 32 query heads, 45.6-46 us, 2.9 TB/s (16 bits 57); 4 of up to 500 cells
+//   7.6-7.9 us, all latency.  Where the stream is not the bound the softmax's instructions
+//   are: two rows at a time in packed arithmetic, and a warp's maximum in one instruction, take
+//   46 us there and 161 on 8 x 65536 cells with heads of 64 (16 bits 162), where single ones
+//   took 49 and 205.  With 16 and 32 rows they are the longer part: 16 query heads to each of 4
+//   KV heads, 8 x 65536 cells, 94 us (16 bits 151); 4 tokens on 32 x up to 4095 65 (62); 8 on
+//   8 x 32768 183 (155).  FP16, with one part more of queries and weights, takes 156 us on 8 x
+//   65536, 50 on 32 x 4095 and 237 for 8 tokens.  Measured on earlier forms and not kept: a
+//   segment's end as 4 units, 343.7 us over five decode steps where 2 take 347.3, but 16 sequences of up to 8000 cells 41.1 where 39.2; MMAs issued by
 //   single threads 72 and 251 us (operands that the compiler does not know to be uniform
 //   cost 150 clocks an MMA); a wait for the room of the weights before the scores 175;
 //   the scales at most two tiles ahead 49 and 158.
@@ -77,7 +81,7 @@ constexpr int W_K = 8, W_V = 9, W_S = 10, W_Q = 11, W_MERGE = 12, W_SCALE = 13, 
 constexpr int kBufs = 4;        // tiles whose scores, and whose weights, have room
 constexpr int kTiles = 8;       // tiles whose scales are at hand
 constexpr int kSegs = 8;        // segments whose rows' scales are at hand
-constexpr int kWeightShift = 9; // products are times 2^9: at most 2^15 with the base's lag
+constexpr float kWeightShift = 9.f; // products are times 2^9: at most 2^15 with their base's lag
 constexpr float kLag = 6.f;
 constexpr float kNone = -1e30f; // a row that has seen no cell: finite, so that no difference is NaN
 
@@ -103,7 +107,7 @@ struct DCfg {
   static constexpr int TS_OFF = P_OFF + kBufs * PBUF;
   static constexpr int RQ_OFF = TS_OFF + kTiles * static_cast<int>(sizeof(KeyScales));  // the rows' scales of kSegs segments
   static constexpr int RED_OFF = RQ_OFF + kSegs * NR * 4;       // [warpgroup][4 warps]: maxima of its rows' scores and products, sums, flag
-  static constexpr int RED = 4 * (3 * HR + 1) * 4;
+  static constexpr int RED = 4 * (3 * HR + 1) * 4;  // (a multiple of 16)
   static constexpr int SCR_OFF = RED_OFF + 2 * RED;             // the schedule's scratch
   static constexpr int SEQ_OFF = SCR_OFF + paged_scratch_bytes(THREADS);
   static constexpr int BAR_OFF = SEQ_OFF + kPagedSeqs * static_cast<int>(sizeof(PagedSeq));
@@ -148,6 +152,13 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const float (&v)[N]) {
   } else {
     tmem_st16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(r));
   }
+}
+
+// The largest of a warp's values; a NaN is none, unless all are.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Whether `p` holds for any thread of the 128 that meet at barrier `id`.
@@ -527,6 +538,10 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
   } else {
     // ------------------------------------------------------------ softmax (warps 0-7)
     constexpr int HR = C::HR;
+    // Pairs of rows whose exponents stay in registers from the vote to the weights; more would
+    // spill (8 tokens on 8 x 32768 cells, 16 rows here, 183 us, 203 with all kept; 16 query heads to
+    // a KV head on 8 x 65536, 8 rows here, 94 us, 116 with none).
+    constexpr int KEPT = HR / 2 < 4 ? HR / 2 : 4;
     const int wg = warp >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;     // of the tile, == TMEM lane; of the result: the column d
     const int row0 = wg * HR;
@@ -537,9 +552,9 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
     float* sums = red_y + 4 * HR;                                           // [4][HR]
     int* red_ok = reinterpret_cast<int*>(sums + 4 * HR);                    // [4]
     const int bar_id = 1 + wg;
-    // Of each row: the base of its weights and their sum, and what the base of its
-    // products has more (a whole number).
-    float m[HR], l[HR], vb[HR];
+    // Of each row (two side by side): the base of its weights, negative, and their sum;
+    // 2^kWeightShift over what the base of its products has more, in exponents (a whole number).
+    float2 nm[HR / 2], l[HR / 2], nv[HR / 2];
     int t = 0;
     // A wait that gave up must not keep this warp from a barrier that the others of its
     // warpgroup come to: it goes on without effect until they leave together.
@@ -547,17 +562,16 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
     for (int seg = 0; walk.ok; walk.advance_segment(), ++seg) {
       const int parts = walk.parts();
 #pragma unroll
-      for (int r = 0; r < HR; ++r) {
-        m[r] = kNone;
-        l[r] = 0.f;
-        vb[r] = 0.f;
+      for (int i = 0; i < HR / 2; ++i) {
+        nm[i] = make_float2(-kNone, -kNone);
+        l[i] = make_float2(0.f, 0.f);
+        nv[i] = make_float2(kWeightShift, kWeightShift);
       }
       const float* rq = q_scale + seg % kSegs * NR + row0;
       for (int k = 0; k < parts; ++k, ++t) {
         const int j = walk.j_first + k, b = t % kBufs;
         alive = alive && KVGQA_WAIT(&s_full[b], (t / kBufs) & 1);
-        bool grow = !alive;
-        float x[HR];
+        float2 x[HR / 2];
         float ev;  // the value's exponent
         tc_fence_after();
         {
@@ -567,41 +581,52 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
           const KeyScales& ks = scales[t % kTiles];
           const float kf = ks.k[key >> kScaleShift] * p.scale_log2;
           ev = ks.v[key >> kScaleShift];
-          float q[HR];
+          float2 q[HR / 2];
 #pragma unroll
-          for (int r = 0; r < HR; r += 4) *reinterpret_cast<float4*>(q + r) = *reinterpret_cast<const float4*>(rq + r);
+          for (int i = 0; i < HR / 2; i += 2) {
+            const float4 w = *reinterpret_cast<const float4*>(rq + 2 * i);
+            q[i] = make_float2(w.x, w.y);
+            q[i + 1] = make_float2(w.z, w.w);
+          }
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < HR; ++r) {
-            float d = fmaf(s[1][r], 0.03125f, s[0][r]);
-            if (C::QP == 3) d = fmaf(s[C::QP - 1][r], 0.0009765625f, d);
-            x[r] = d * (kf * q[r]);
+          for (int i = 0; i < HR / 2; ++i) {
+            auto part = [&](int k) { return make_float2(s[k][2 * i], s[k][2 * i + 1]); };
+            float2 d = ffma2(part(1), make_float2(0.03125f, 0.03125f), part(0));
+            if (C::QP == 3) d = ffma2(part(C::QP - 1), make_float2(0.0009765625f, 0.0009765625f), d);
+            x[i] = fmul2(d, fmul2(make_float2(kf, kf), q[i]));
           }
         }
         const int cell = j * BN + key;
         if ((j + 1) * BN > walk.off + 1) {   // a tile that reaches past a row's cell: row r sees those up to off + its token
 #pragma unroll
           for (int r = 0; r < HR; ++r)
-            if (cell > min(walk.off + ((row0 + r) >> p.gp_shift), walk.kend - 1)) x[r] = -INFINITY;
+            if (cell > min(walk.off + ((row0 + r) >> p.gp_shift), walk.kend - 1)) (r & 1 ? x[r / 2].y : x[r / 2].x) = -INFINITY;
         }
+        // The exponents of two rows' weights, and of their products with the value's scale.
+        auto weight2 = [&](int i) { return fadd2(x[i], nm[i]); };
+        auto product2 = [&](int i, float2 w) { return fadd2(w, fadd2(make_float2(ev, ev), nv[i])); };
+        float2 w[KEPT], y[KEPT];
+        float most_w = -INFINITY, most_y = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < HR; ++r) {
-          const float t = x[r] - m[r];
-          grow = grow || fmaxf(t, t + (ev - vb[r])) > kLag;
+        for (int i = 0; i < HR / 2; ++i) {
+          const float2 wi = weight2(i), yi = product2(i, wi);
+          if (i < KEPT) {
+            w[i] = wi;
+            y[i] = yi;
+          }
+          most_w = fmax3(most_w, wi.x, wi.y);
+          most_y = fmax3(most_y, yi.x, yi.y);
         }
-        if (vote_any(bar_id, grow)) {
+        if (vote_any(bar_id, !alive || most_w > kLag || most_y > kWeightShift + kLag)) {
           // The maxima of the tile, over the warpgroup.
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
-            float v = x[r], y = x[r] + ev;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-              v = fmaxf(v, __shfl_xor_sync(FULLMASK, v, o));
-              y = fmaxf(y, __shfl_xor_sync(FULLMASK, y, o));
-            }
+            const float xr = r & 1 ? x[r / 2].y : x[r / 2].x;
+            const float v = warp_max(xr), y = warp_max(xr + ev);
             if (lane == 0) {
-              red[quarter * HR + r] = v;
-              red_y[quarter * HR + r] = y;
+              red[r * 4 + quarter] = v;
+              red_y[r * 4 + quarter] = y;
             }
           }
           if (lane == 0) red_ok[quarter] = alive;
@@ -616,17 +641,25 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
           float alpha[HR];
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
-            const float top = fmaxf(fmaxf(red[r], red[HR + r]), fmaxf(red[2 * HR + r], red[3 * HR + r]));
-            const float top_y = fmaxf(fmaxf(red_y[r], red_y[HR + r]), fmaxf(red_y[2 * HR + r], red_y[3 * HR + r]));
+            const float4 tx = *reinterpret_cast<const float4*>(red + 4 * r), ty = *reinterpret_cast<const float4*>(red_y + 4 * r);
+            const float top = fmaxf(fmaxf(tx.x, tx.y), fmaxf(tx.z, tx.w)), top_y = fmaxf(fmaxf(ty.x, ty.y), fmaxf(ty.z, ty.w));
             // (A row that has seen no cell, or none with a scale, has a base near kNone, and
             // zeros so far.  The products' base falls by less than a binade where the
             // weights' alone grows, else it does not fall; as the latter is a maximum here, the
             // difference is 254 at most.)
-            const float to = fmaxf(m[r], top), by = floorf(fmaxf(m[r] + vb[r], top_y) - to), a = m[r] - to;
-            alpha[r] = ex2(fminf(a + (vb[r] - by), 1.f));
-            l[r] *= ex2(a);
-            m[r] = to;
-            vb[r] = by;
+            float& nmr = r & 1 ? nm[r / 2].y : nm[r / 2].x;
+            float& nvr = r & 1 ? nv[r / 2].y : nv[r / 2].x;
+            const float m = -nmr, vb = kWeightShift - nvr;
+            const float to = fmaxf(m, top), by = floorf(fmaxf(m + vb, top_y) - to), a = m - to;
+            alpha[r] = ex2(fminf(a + (vb - by), 1.f));
+            (r & 1 ? l[r / 2].y : l[r / 2].x) *= ex2(a);
+            nmr = -to;
+            nvr = kWeightShift - by;
+          }
+#pragma unroll
+          for (int i = 0; i < KEPT; ++i) {
+            w[i] = weight2(i);
+            y[i] = product2(i, w[i]);
           }
           if (move) {
             tc_fence_after();
@@ -647,10 +680,10 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
         if (t >= kBufs) alive = alive && KVGQA_WAIT(&o_done[b], (t / kBufs - 1) & 1);  // the buffer's last weights have been used
 #pragma unroll
         for (int r = 0; r < HR; r += 2) {
-          const float t0 = x[r] - m[r], t1 = x[r + 1] - m[r + 1];
-          l[r] += ex2(t0);
-          l[r + 1] += ex2(t1);
-          __half2 h = __floats2half2_rn(ex2(t0 + (ev - vb[r] + kWeightShift)), ex2(t1 + (ev - vb[r + 1] + kWeightShift)));
+          const int i = r / 2;
+          const float2 wi = i < KEPT ? w[i < KEPT ? i : 0] : weight2(i), yi = i < KEPT ? y[i < KEPT ? i : 0] : product2(i, wi);
+          l[i] = fadd2(l[i], make_float2(ex2(wi.x), ex2(wi.y)));
+          __half2 h = __floats2half2_rn(ex2(yi.x), ex2(yi.y));
 #pragma unroll
           for (int part = 0; part < C::PP; ++part) {
             const uint32_t c = (*reinterpret_cast<const uint32_t*>(&h) + 0x00800080u) & 0xff00ff00u;
@@ -670,7 +703,7 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       // ---------------------------------------------------------- end of this part of the segment
 #pragma unroll
       for (int r = 0; r < HR; ++r) {
-        float v = l[r];
+        float v = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULLMASK, v, o);
         if (lane == 0) sums[quarter * HR + r] = v;
@@ -681,7 +714,7 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       const int rows = min(walk.ql << p.gp_shift, NR);
       const bool whole = walk.whole(), starts = walk.vlo >= walk.v0;
       float* slot = p.partials + (static_cast<size_t>(blockIdx.x) * 2 + starts) * part_floats(D);
-      float o[HR];
+      float o[HR], sum[HR], m[HR];
 #pragma unroll
       for (int r = 0; r < HR; ++r) o[r] = 0.f;
 #pragma unroll
@@ -694,9 +727,11 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
       }
 #pragma unroll
       for (int r = 0; r < HR; ++r) {
-        l[r] = sums[r] + sums[HR + r] + sums[2 * HR + r] + sums[3 * HR + r];
+        sum[r] = sums[r] + sums[HR + r] + sums[2 * HR + r] + sums[3 * HR + r];
+        m[r] = -(r & 1 ? nm[r / 2].y : nm[r / 2].x);
+        const float vb = kWeightShift - (r & 1 ? nv[r / 2].y : nv[r / 2].x);
         // (the products' base in two steps: by itself it may be below FP32's range)
-        o[r] = o[r] * pow2(-kWeightShift) * pow2(static_cast<int>(fmaxf(vb[r], -1000.f)) - 127);
+        o[r] = o[r] * 0x1p-9f * pow2(static_cast<int>(fmaxf(vb, -1000.f)) - 127);
       }
       if (alive) {
 #pragma unroll
@@ -705,13 +740,13 @@ paged_decode_e4m3_kernel(const __grid_constant__ PagedAttentionParams p, const _
           if (row >= rows || gi >= p.G) continue;
           if (whole) {
             const size_t head = static_cast<size_t>(walk.first + (row >> p.gp_shift)) * p.H_q + walk.g * p.G + gi;
-            if (D == 128 || key < D) p.out[head * D + key] = E::from_f32(o[r] * __fdividef(1.f, l[r]));
-            if (key == 0 && p.lse) p.lse[head] = (m[r] + log2f(l[r])) * 0.6931471805599453f;
+            if (D == 128 || key < D) p.out[head * D + key] = E::from_f32(o[r] * __fdividef(1.f, sum[r]));
+            if (key == 0 && p.lse) p.lse[head] = (m[r] + log2f(sum[r])) * 0.6931471805599453f;
           } else {
             if (D == 128 || key < D) slot[row * D + key] = o[r];
             if (key == 0) {
               slot[kSmallRows * D + row] = m[r];
-              slot[kSmallRows * (D + 1) + row] = l[r];
+              slot[kSmallRows * (D + 1) + row] = sum[r];
             }
           }
         }
