@@ -1117,7 +1117,7 @@ cudaError_t make_maps(const PagedAttentionParams& p, Maps* m) {
   const cuuint64_t D = p.D, G = p.G, Hkv = p.H_kv;
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const cuuint32_t gp = 1u << p.gp_shift;
-  for (int t = 0; t < 2; ++t) {  // q, and out in boxes of 32 rows
+  for (int t = 0; t < (kE4M3 ? 1 : 2); ++t) {  // q, and out in boxes of 32 rows (with codes out takes direct stores)
     const cuuint64_t dims[4] = {D, G, Hkv, static_cast<cuuint64_t>(p.m.N)};
     const cuuint64_t strides[3] = {D * 2, D * 2 * G, D * 2 * G * Hkv};
     const cuuint32_t box[4] = {64, gp, 1, t == 0 ? static_cast<cuuint32_t>(p.box_tokens) : 32 / gp};
@@ -1221,7 +1221,7 @@ cudaError_t launch_paged_attention_e4m3_chunks(const PagedAttentionParams& param
   p.box_tokens = 1;
   while (p.box_tokens << p.gp_shift < BM && p.box_tokens < p.m.max_query_len) p.box_tokens *= 2;
   p.end_units = is_small(p) ? 2 : kE4M3 ? 6 : 4;
-  Maps m;
+  Maps m{};
   const cudaError_t e = make_maps(p, &m);
   if (e != cudaSuccess) return e;
   if (p.D == 128) return launch_width<128>(p, m, stream);
