@@ -213,7 +213,7 @@ __device__ __forceinline__ void merge_small(const PagedAttentionParams& p, int t
 // takes the scales out again, in FP32.
 //
 // What bounds it: 4 chunks of 2048 tokens after 6000-14000 cells take 1800 us, 0.81
-// PFLOP/s, where the 16-bit cache takes 1105, a mixed step of 28 sequences 148 (98): the
+// PFLOP/s, where the 16-bit cache takes 1105-1120, a mixed step of 28 sequences 145 (95): the
 // softmax of a tile beside the MMAs, 2048 clocks of a round of two tiles (its scales are
 // more registers, exponentials and reads of shared memory, and the code of four roles passes
 // through the instruction cache), and the four expanding warps beside it.  Before the values'

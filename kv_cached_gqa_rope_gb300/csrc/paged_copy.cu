@@ -5,7 +5,7 @@
 // short.  A warp copies 4 KB of one page of one pool, 8 loads of 16 bytes a
 // lane in flight before the first store; the warp of a page's first 4 KB takes the
 // page's scales along.  8192 pages of 32 cells (8 KV heads of 128, codes; 1.07 GB moved)
-// take 161 us, 6.67 TB/s, 98 % of a copy's rate; 507 of 4 heads of 64 in FP16 6.1 us, 82 %;
+// take 161 us, 6.67 TB/s, 98 % of a copy's rate; 507 of 4 heads of 64 in FP16 5.8-6.1 us, 80-84 %;
 // 16 pages 2.0 us in a graph, 4.1 in calls.
 #include <cuda_runtime.h>
 
